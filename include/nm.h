@@ -550,6 +550,102 @@ nm_status nm_spense_outsplit_gemm(const void* x, int64_t t, int64_t k, int64_t l
                                   int64_t workspace_bytes, void* stream);
 int64_t nm_spense_outsplit_workspace_size(int64_t t, int64_t k, int64_t o_s, int64_t o_d);
 
+/*
+ * ------------------------------------------------------------------------------------
+ * 8-bit integer layers.  [SLIDE] 2.B-2.C serves INT8: activations quantized per token (and
+ * lifted) in one pass, then the 2:4 product in 8-bit integers.  Both operands are int8 codes
+ * with one fp32 scale per row (token of X, output channel of W), sums are exact 32-bit
+ * integers, and y = (fp32(sum) * x_scale[t]) * w_scale[o].
+ *
+ * Code rows are leading-dimension BYTES apart (a multiple of 16, >= the row length); every
+ * byte of a row is readable, and the bytes of an X row from k up to the next multiple of
+ * 16 are ZERO, as nm_quant_i8 writes them (those of W may hold anything).  Codes span
+ * [-128, 127] (nm_quant_i8 writes [-127, 127]).  Reduction lengths up to NM_I8_MAX_K keep
+ * every sum inside 32 bits; longer ones return NM_EUNSUPPORTED.
+ */
+#define NM_I8_MAX_K 131071
+
+/*
+ * nm_quant_i8 -- rows of bf16 to int8 codes and one scale per row: the activations of a
+ * token, or (once, offline) the weights of an output channel, compressed 2:4 values included.
+ *   amax = max_k |x[r][k]|,  scale[r] = fp32(amax / 127)  (1 if amax = 0)
+ *   q[r][k] = 127 x[r][k] / amax, the exact quotient rounded to the nearest integer, ties to
+ *             even (0 if amax = 0); with a pattern (m > 0) 0 where S_{n:m} drops x[r][k]
+ * The selection is nm_sparsify's ([FLEX] 2.A, 2.C) and always keeps the row's largest value.
+ * A row that holds an infinity or a NaN gets the scale inf or NaN and all-zero codes, so every
+ * product of it is NaN.  With ns in 3..8 the codes are written lifted for (2N-2):2N weights
+ * (N = ns, [SLIDE] 2.B): q'[r][g*4(N-1) + 4w + s] = q[r][g*2N + 2w + s], K' = k(2N-2)/N.
+ *   x      bf16 [rows][ldx], ldx % 8 == 0
+ *   n, m   m = 0: no selection (n is not read); m in {4, 8, 16, 32}: 1 <= n <= m, k % m == 0
+ *   ns     2: no lift; 3..8: k % (2 ns) == 0 (not together with a selection: NM_EUNSUPPORTED)
+ *   q      int8 [rows][ldq], ldq % 16 == 0, ldq >= the row length rounded up to 16; codes past
+ *          the row length up to that multiple are written 0, bytes beyond it are left alone
+ *   scale  fp32 [rows]
+ * k <= 65536 (NM_EUNSUPPORTED above).  q must not overlap x.  Results are bit-exact.
+ */
+nm_status nm_quant_i8(const void* x, int64_t rows, int64_t k, int64_t ldx, int n, int m, int ns, int8_t* q,
+                      int64_t ldq, float* scale, void* stream);
+
+/*
+ * nm_meta_block -- 2-bit positions of a 2:4 weight from rows ([o][ceil(kc/8)] bytes, as
+ * nm_compress and nm_lower_slide write them) to the step blocks the int8 products read:
+ * out [ceil(kc/128)][o][16 bytes], block s holding every row's positions of values
+ * [64s, 64s + 64).  Slots past the row are filled with the positions 0, 1.  Offline, once per
+ * weight.  kc % 4 == 0; out takes nm_meta_block_bytes(o, kc) bytes and must not overlap meta.
+ */
+nm_status nm_meta_block(const void* meta, int64_t o, int64_t kc, void* out, void* stream);
+int64_t nm_meta_block_bytes(int64_t o, int64_t kc);
+
+typedef enum { NM_Y_F32 = 0, NM_Y_BF16 = 1 } nm_ydtype;
+
+/*
+ * nm_spmm_i8 -- the linear layer in 8-bit integers:
+ *   Y[t][o] (=|+=) (fp32(sum_k x[t][k] w[o][k]) * x_scale[t]) * w_scale[o] + beta_t * col_shift[o]
+ *   x        int8 [t][ldx], x_scale fp32 [t]  (nm_quant_i8 of the activations; lifted codes and
+ *            k = K' for lowered weights)
+ *   w        w_meta NULL: int8 [o][ldw], dense, any k.  Otherwise 2:4 over k (k % 4 == 0): the
+ *            kept values' codes int8 [o][ldw >= k/2] in nm_compress's order, w_meta the
+ *            positions in step blocks (nm_meta_block); on the sparse matrix instruction.
+ *   w_scale  fp32 [o]
+ *   row_shift, col_shift   optional term: beta_t = row_shift[t], 1 when NULL (then col_shift
+ *            is a bias); row_shift needs col_shift (NM_EINVAL)
+ *   y        NM_Y_F32: fp32 [t][ldy], NM_Y_BF16: bf16 [t][ldy] (rounded once, to nearest even);
+ *            any ldy >= o; accumulate (Y += result) with NM_Y_F32 only (NM_EUNSUPPORTED)
+ *   workspace  device scratch or NULL.  With nm_i8_workspace_size bytes the reduction may be
+ *            split across workgroups; with less, the call runs unsplit.  Contents after the
+ *            call are unspecified; calls sharing a workspace must be ordered.
+ *   route    NM_ROUTE_FEW_STREAM, NM_ROUTE_FEW_TILE, NM_ROUTE_TILE_LDS force the streaming, the
+ *            split-tile and the large-tile kernel; other bits are ignored, 0 = by shape
+ *   route_taken  host pointer or NULL: NM_TAKEN_* bits of what ran (OR-ed in)
+ * k == 0 gives zero sums (x and w may then be NULL).  The sums are exact, so every route gives
+ * the same bits.  Nothing outside rows [0, t) and columns [0, o) of y is written.
+ */
+nm_status nm_spmm_i8(const int8_t* x, int64_t t, int64_t k, int64_t ldx, const float* x_scale, const int8_t* w,
+                     int64_t o, int64_t ldw, const float* w_scale, const void* w_meta, const float* row_shift,
+                     const float* col_shift, void* y, int64_t ldy, nm_ydtype y_dtype, int accumulate,
+                     void* workspace, int64_t workspace_bytes, uint32_t route, uint32_t* route_taken,
+                     void* stream);
+
+typedef enum { NM_GLU_SILU = 0, NM_GLU_GELU_TANH = 1 } nm_glu_act;
+
+/*
+ * nm_glu_i8 -- the gate and up products of a GLU MLP ([SPENSE] 2.A: down(act(gate x) * up x))
+ * in one pass:
+ *   g = (fp32(sum_k x[t][k] w_gate[i][k]) * x_scale[t]) * gate_scale[i], u likewise from w_up
+ *   Y[t][i] = act(g) * u,  NM_GLU_SILU: g / (1 + e^-g),
+ *                          NM_GLU_GELU_TANH: g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2
+ * Both weights are dense (gate_meta and up_meta NULL) or both 2:4 (NM_EINVAL otherwise), with
+ * the layouts, the leading dimension and the rules of nm_spmm_i8; no accumulation, no shift.
+ */
+nm_status nm_glu_i8(const int8_t* x, int64_t t, int64_t k, int64_t ldx, const float* x_scale, const int8_t* w_gate,
+                    const float* gate_scale, const void* gate_meta, const int8_t* w_up, const float* up_scale,
+                    const void* up_meta, int64_t inter, int64_t ldw, nm_glu_act act, void* y, int64_t ldy,
+                    nm_ydtype y_dtype, void* workspace, int64_t workspace_bytes, uint32_t route,
+                    uint32_t* route_taken, void* stream);
+
+/* Workspace bytes of the preferred route of nm_spmm_i8 (glu = 0) or nm_glu_i8 (glu = 1). */
+int64_t nm_i8_workspace_size(int64_t t, int64_t o, int64_t k, int sparse, int glu, uint32_t route);
+
 #ifdef __cplusplus
 }
 #endif

@@ -764,3 +764,73 @@ def spmm_pts(x_bits, w_bits, n: int, m: int, mode: int, static_shift=None, col_s
         beta = mu.astype(np.float64)[:, None] if mode & PTS_DYNAMIC else 1.0
         y = y + beta * v
     return y, s, keep, mu, alpha
+
+
+# --------------------------------------------------------------------------- int8 layers
+# The INT8 form of the layer ([SLIDE] 2.B-2.C names INT8 serving; the page gives no scheme):
+# symmetric absmax codes per row, exact integer sums, both scales applied to the sum.
+
+def quantize_rows_i8(x_bits: np.ndarray, n: int = 0, m: int = 0, ns: int = 2):
+    """Rows of bf16 -> (int8 codes [R][K or K'], fp32 scales [R]).  amax = max |x| of the row,
+    scale = fp32(amax / 127), code = 127 x / amax rounded to the nearest integer, ties to
+    even; the quotient is formed in fp64, where every tie is exact and every other value (at
+    most 15 over 8 significant bits) stays on its side.  m > 0: codes outside S_{n:m} are 0.
+    ns > 2: codes lifted.  An all-zero row has scale 1; a row with an infinity or a NaN has
+    that as its scale (NaN above infinity) and zero codes."""
+    x_bits = np.asarray(x_bits, np.uint16)
+    rows, k = x_bits.shape
+    key = magnitude_key(x_bits).max(axis=1) if k else np.zeros(rows, np.uint16)
+    amax = bf16_to_f64(np.asarray(key, np.uint16))
+    bad = np.asarray(key, np.int64) >= 0x7F80
+    usable = ~bad & (amax > 0)
+    safe = np.where(usable, amax, 1.0)
+    vals = np.where(usable[:, None], bf16_to_f64(np.where(usable[:, None], x_bits, 0)), 0.0)
+    codes = np.rint(127.0 * vals / safe[:, None]).astype(np.int8)
+    if m:
+        codes = np.where(select_keep(x_bits, n, m), codes, np.int8(0))
+    scale = np.where(bad, amax, np.where(amax > 0, safe / 127.0, 1.0)).astype(np.float32)
+    if ns > 2:
+        codes = lift(codes.astype(np.int8).view(np.uint8).astype(np.uint16), ns).astype(np.uint8).view(np.int8)
+    return codes, scale
+
+
+def block_meta(meta: np.ndarray, kc: int) -> np.ndarray:
+    """2-bit positions [O][ceil(kc/8)] -> step blocks [ceil(kc/128)][O][16], slots past the row
+    filled with the positions 0, 1 (byte 0x44)."""
+    o = meta.shape[0]
+    steps = -(-kc // 128)
+    out = np.full((steps, o, 16), 0x44, np.uint8)
+    for r in range(o):
+        for b in range(meta.shape[1]):
+            v = int(meta[r, b])
+            if 8 * (b + 1) > kc:
+                v = (v & 0x0F) | 0x40
+            out[b // 16, r, b % 16] = v
+    return out
+
+
+def expand_24(codes: np.ndarray, idx: np.ndarray, kc: int) -> np.ndarray:
+    """2:4 codes [O][kc/2] with in-group positions idx (same shape) -> dense [O][kc] int64."""
+    o = codes.shape[0]
+    w = np.zeros((o, kc), np.int64)
+    for j in range(kc // 2):
+        w[np.arange(o), 4 * (j // 2) + idx[:, j].astype(np.int64)] = codes[:, j]
+    return w
+
+
+def sums_i8(x: np.ndarray, w: np.ndarray) -> np.ndarray:
+    """Exact integer products sum_k x[t][k] w[o][k] (every partial sum below 2^53 in fp64)."""
+    return x.astype(np.float64) @ w.astype(np.float64).T
+
+
+def scaled_i8(sums: np.ndarray, x_scale: np.ndarray, w_scale: np.ndarray) -> np.ndarray:
+    """sums[t][o] * x_scale[t] * w_scale[o] in fp64."""
+    return sums * np.asarray(x_scale, np.float64)[:, None] * np.asarray(w_scale, np.float64)[None, :]
+
+
+def glu_gate(g: np.ndarray, act: str) -> np.ndarray:
+    """silu: g / (1 + e^-g); gelu (tanh form): g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2,
+    by 1 + tanh z = 2 / (1 + e^-2z), in fp64."""
+    z = g if act == "silu" else 2.0 * np.sqrt(2.0 / np.pi) * (g + 0.044715 * g ** 3)
+    with np.errstate(over="ignore"):
+        return g / (1.0 + np.exp(-z))

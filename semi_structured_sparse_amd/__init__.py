@@ -25,7 +25,8 @@ __all__ = [
     "nm_spense_glu_order_workspace_size", "nm_spense_pack", "nm_spense_pack_workspace_size",
     "nm_spense_outsplit_gemm", "nm_spense_outsplit_workspace_size", "nm_quant_lift", "NM_PTS_DYNAMIC",
     "NM_PTS_STATIC", "NM_PTS_VAR", "nm_sparsify_pts", "nm_weight_sums", "NM_ESCRATCH", "nm_spmm_noalloc",
-    "NM_NOALLOC_SCRATCH_BYTES",
+    "NM_NOALLOC_SCRATCH_BYTES", "nm_quant_i8", "nm_meta_block", "nm_meta_block_bytes", "nm_spmm_i8", "nm_glu_i8",
+    "nm_i8_workspace_size", "NM_I8_MAX_K", "NM_Y_F32", "NM_Y_BF16", "NM_GLU_SILU", "NM_GLU_GELU_TANH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnmsparse.so")
@@ -38,6 +39,9 @@ NM_SCORE_ACT_WEIGHTED, NM_SCORE_WEIGHT = 0, 1
 NM_SPENSE_LOSS, NM_SPENSE_TAIL = 0, 1
 NM_ACT_DYNAMIC, NM_ACT_COMPRESSED, NM_W_COMPRESSED, NM_W_SLIDE, NM_ACT_MASKED = range(5)
 NM_PTS_DYNAMIC, NM_PTS_STATIC, NM_PTS_VAR = 1, 2, 4
+NM_I8_MAX_K = 131071
+NM_Y_F32, NM_Y_BF16 = 0, 1
+NM_GLU_SILU, NM_GLU_GELU_TANH = 0, 1
 
 # route hints (NM_ROUTE_*) and the report of what ran (NM_TAKEN_*), by lower-case name
 ROUTE = {name: 1 << i for i, name in enumerate(
@@ -150,6 +154,20 @@ def lib() -> ctypes.CDLL:
                                           _vp, _i64, _vp]
     L.nm_spense_outsplit_workspace_size.restype = _i64
     L.nm_spense_outsplit_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
+    L.nm_quant_i8.restype = _int
+    L.nm_quant_i8.argtypes = [_vp, _i64, _i64, _i64, _int, _int, _int, _vp, _i64, _vp, _vp]
+    L.nm_meta_block.restype = _int
+    L.nm_meta_block.argtypes = [_vp, _i64, _i64, _vp, _vp]
+    L.nm_meta_block_bytes.restype = _i64
+    L.nm_meta_block_bytes.argtypes = [_i64, _i64]
+    L.nm_spmm_i8.restype = _int
+    L.nm_spmm_i8.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _int, _int,
+                             _vp, _i64, ctypes.c_uint32, _vp, _vp]
+    L.nm_glu_i8.restype = _int
+    L.nm_glu_i8.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _vp, _i64,
+                            _int, _vp, _i64, ctypes.c_uint32, _vp, _vp]
+    L.nm_i8_workspace_size.restype = _i64
+    L.nm_i8_workspace_size.argtypes = [_i64, _i64, _i64, _int, _int, ctypes.c_uint32]
     _LIB = L
     return L
 
@@ -443,4 +461,76 @@ def nm_hybrid_gemm(x, sparse_cols, k_s, dense_cols, k_d, ws_values, ws_meta, fmt
                               ctypes.addressof(taken) if taken is not None else None, _stream(stream))
     if check:
         _check(st, "nm_hybrid_gemm")
+    return st
+
+
+# ------------------------------------------------------------------------ int8 layers ---
+
+def _i8_out(y):
+    """NM_Y_* of an output tensor (raw pointers: fp32)."""
+    return NM_Y_BF16 if not isinstance(y, int) and y is not None and y.element_size() == 2 else NM_Y_F32
+
+
+def _bytes(t):
+    return 0 if t is None or isinstance(t, int) else t.numel() * t.element_size()
+
+
+def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, ldx=None, ldq=None, check=True):
+    rows = x.shape[0] if rows is None else rows
+    k = x.shape[1] if k is None else k
+    st = lib().nm_quant_i8(_ptr(x), rows, k, _ld(x) if ldx is None else ldx, n, m, ns, _ptr(q),
+                           _ld(q) if ldq is None else ldq, _ptr(scale), _stream(stream))
+    if check:
+        _check(st, "nm_quant_i8")
+    return st
+
+
+def nm_meta_block(meta, o, kc, out, stream=None, *, check=True):
+    st = lib().nm_meta_block(_ptr(meta), o, kc, _ptr(out), _stream(stream))
+    if check:
+        _check(st, "nm_meta_block")
+    return st
+
+
+def nm_meta_block_bytes(o: int, kc: int) -> int:
+    return int(lib().nm_meta_block_bytes(o, kc))
+
+
+def nm_i8_workspace_size(t: int, o: int, k: int, sparse: bool = False, glu: bool = False, route: int = 0) -> int:
+    return int(lib().nm_i8_workspace_size(t, o, k, 1 if sparse else 0, 1 if glu else 0, route))
+
+
+def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift=None, accumulate=0, workspace=None,
+               stream=None, *, t=None, o=None, k=None, ldx=None, ldw=None, ldy=None, y_dtype=None,
+               workspace_bytes=None, route=0, taken=None, check=True):
+    """taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
+    st = lib().nm_spmm_i8(_ptr(x), x.shape[0] if t is None else t, x.shape[1] if k is None else k,
+                          _ld(x) if ldx is None else ldx, _ptr(x_scale), _ptr(w), w.shape[0] if o is None else o,
+                          _ld(w) if ldw is None else ldw, _ptr(w_scale), _ptr(w_meta), _ptr(row_shift),
+                          _ptr(col_shift), _ptr(y), _ld(y) if ldy is None else ldy,
+                          _i8_out(y) if y_dtype is None else y_dtype, accumulate, _ptr(workspace),
+                          _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
+                          ctypes.addressof(taken) if taken is not None else None, _stream(stream))
+    if check:
+        _check(st, "nm_spmm_i8")
+    return st
+
+
+def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU, gate_meta=None, up_meta=None,
+              workspace=None, stream=None, *, t=None, inter=None, k=None, ldx=None, ldw=None, ldy=None, y_dtype=None,
+              workspace_bytes=None, route=0, taken=None, check=True):
+    """taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
+    if ldw is None:
+        ldw = _ld(w_gate)
+        if _ld(w_up) != ldw:
+            raise ValueError("w_gate and w_up need the same leading dimension")
+    st = lib().nm_glu_i8(_ptr(x), x.shape[0] if t is None else t, x.shape[1] if k is None else k,
+                         _ld(x) if ldx is None else ldx, _ptr(x_scale), _ptr(w_gate), _ptr(gate_scale),
+                         _ptr(gate_meta), _ptr(w_up), _ptr(up_scale), _ptr(up_meta),
+                         w_gate.shape[0] if inter is None else inter, ldw, act, _ptr(y),
+                         _ld(y) if ldy is None else ldy, _i8_out(y) if y_dtype is None else y_dtype, _ptr(workspace),
+                         _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
+                         ctypes.addressof(taken) if taken is not None else None, _stream(stream))
+    if check:
+        _check(st, "nm_glu_i8")
     return st

@@ -1,0 +1,129 @@
+// C ABI of the int8 layers: host-side validation and dispatch (nm_quant_i8, nm_meta_block,
+// nm_spmm_i8, nm_glu_i8).  Arguments are checked completely before the first HIP call.
+#include "i8_launch.h"
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// rows x ld elements of up to 8 bytes addressable in 64 bits
+bool span_ok(int64_t rows, int64_t ld) {
+  int64_t e, b;
+  return rows >= 0 && ld >= 0 && !__builtin_mul_overflow(rows, ld, &e) && !__builtin_mul_overflow(e, (int64_t)8, &b);
+}
+
+nm_status hip_status(hipError_t e) { return e == hipSuccess ? NM_OK : NM_EHIP; }
+
+int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
+
+// a product's arguments (nm_spmm_i8 and nm_glu_i8 alike)
+nm_status check_i8(const nml::I8Args& a, const void* ws, int64_t ws_bytes) {
+  if (a.t < 0 || a.o < 0 || a.k < 0 || ws_bytes < 0) return NM_ESHAPE;
+  if (a.epi.bf16_out != NM_Y_F32 && a.epi.bf16_out != NM_Y_BF16) return NM_EINVAL;
+  if (a.epi.accumulate != 0 && a.epi.accumulate != 1) return NM_EINVAL;
+  if (a.epi.row_shift != nullptr && a.epi.col_shift == nullptr) return NM_EINVAL;
+  const bool glu = a.glu != 0;
+  if (glu && (a.meta != nullptr) != (a.up_meta != nullptr)) return NM_EINVAL;
+  if (a.t > 0 && a.o > 0) {
+    if (a.epi.y == nullptr || a.epi.x_scale == nullptr || a.epi.w_scale == nullptr) return NM_EINVAL;
+    if (glu && a.epi.up_scale == nullptr) return NM_EINVAL;
+    if (a.k > 0 && (a.x == nullptr || a.w == nullptr || (glu && a.w_up == nullptr))) return NM_EINVAL;
+  }
+  const bool sp = a.meta != nullptr;
+  if (sp && a.k % 4 != 0) return NM_ESHAPE;
+  const int64_t wlen = sp ? a.k / 2 : a.k;
+  if (a.ldx < a.k || a.ldw < wlen || a.epi.ldy < a.o) return NM_ESHAPE;
+  if (!span_ok(a.t, a.ldx) || !span_ok(a.o, a.ldw) || !span_ok(a.t, a.epi.ldy) || !span_ok(a.t, a.o)) return NM_ESHAPE;
+  if (sp && !span_ok(a.o, a.k)) return NM_ESHAPE;
+  if (a.ldx % 16 != 0 || a.ldw % 16 != 0) return NM_EALIGN;
+  const void* ptrs[] = {a.x, a.w, a.w_up, a.meta, a.up_meta, a.epi.x_scale, a.epi.w_scale, a.epi.up_scale,
+                        a.epi.row_shift, a.epi.col_shift, a.epi.y, ws};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return NM_EALIGN;
+  if (a.k > NM_I8_MAX_K) return NM_EUNSUPPORTED;
+  if (a.epi.accumulate && a.epi.bf16_out) return NM_EUNSUPPORTED;
+  if (a.t > 0x7FFFFFFF || a.o > 0x7FFFFFFF) return NM_EUNSUPPORTED;
+  return NM_OK;
+}
+
+nm_status run_i8(const nml::I8Args& a, void* ws, int64_t ws_bytes, hipStream_t s) {
+  if (a.t == 0 || a.o == 0) return NM_OK;
+  return hip_status(nml::launch_i8_few(a, static_cast<int32_t*>(ws), ws_bytes, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+nm_status nm_quant_i8(const void* x, int64_t rows, int64_t k, int64_t ldx, int n, int m, int ns, int8_t* q,
+                      int64_t ldq, float* scale, void* stream) {
+  if (m != 0 && m != 4 && m != 8 && m != 16 && m != 32) return m < 0 ? NM_EINVAL : NM_EUNSUPPORTED;
+  if (m != 0 && (n < 1 || n > m)) return NM_EINVAL;
+  if (ns < 2 || ns > 8) return NM_EINVAL;
+  if (m != 0 && ns != 2) return NM_EUNSUPPORTED;
+  if (rows < 0 || k < 0) return NM_ESHAPE;
+  if (m != 0 && k % m != 0) return NM_ESHAPE;
+  if (ns > 2 && k % (2 * ns) != 0) return NM_ESHAPE;
+  if (rows > 0 && (scale == nullptr || (k > 0 && (x == nullptr || q == nullptr)))) return NM_EINVAL;
+  const int64_t kq = ns > 2 ? k / (2 * ns) * 4 * (ns - 1) : k;
+  if (ldx < k || ldq < up16(kq)) return NM_ESHAPE;
+  if (!span_ok(rows, ldx) || !span_ok(rows, ldq)) return NM_ESHAPE;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(scale) || ldx % 8 != 0 || ldq % 16 != 0) return NM_EALIGN;
+  if (k > 65536 || rows > 0x7FFFFFFF) return NM_EUNSUPPORTED;
+  return hip_status(nml::launch_quant_i8(static_cast<const uint16_t*>(x), rows, k, ldx, n, m, ns, q, ldq, scale,
+                                         reinterpret_cast<hipStream_t>(stream)));
+}
+
+int64_t nm_meta_block_bytes(int64_t o, int64_t kc) {
+  if (o <= 0 || kc <= 0 || !span_ok(o, kc)) return 0;
+  return (kc + 127) / 128 * o * 16;
+}
+
+nm_status nm_meta_block(const void* meta, int64_t o, int64_t kc, void* out, void* stream) {
+  if (o < 0 || kc < 0 || kc % 4 != 0 || !span_ok(o, kc)) return NM_ESHAPE;
+  if (o > 0 && kc > 0 && (meta == nullptr || out == nullptr)) return NM_EINVAL;
+  if (!aligned16(meta) || !aligned16(out)) return NM_EALIGN;
+  return hip_status(nml::launch_meta_step_block(static_cast<const uint8_t*>(meta), o, kc, static_cast<uint8_t*>(out),
+                                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+nm_status nm_spmm_i8(const int8_t* x, int64_t t, int64_t k, int64_t ldx, const float* x_scale, const int8_t* w,
+                     int64_t o, int64_t ldw, const float* w_scale, const void* w_meta, const float* row_shift,
+                     const float* col_shift, void* y, int64_t ldy, nm_ydtype y_dtype, int accumulate,
+                     void* workspace, int64_t workspace_bytes, uint32_t route, uint32_t* route_taken,
+                     void* stream) {
+  nml::I8Args a{};
+  a.x = x; a.ldx = ldx; a.w = w; a.ldw = ldw; a.meta = static_cast<const uint8_t*>(w_meta);
+  a.t = t; a.o = o; a.k = k;
+  a.epi = nml::I8Epi{x_scale, w_scale, nullptr, row_shift, col_shift, y, ldy, (int)y_dtype, accumulate, 0};
+  a.route.flags = route;
+  a.route.taken = route_taken;
+  const nm_status st = check_i8(a, workspace, workspace_bytes);
+  return st != NM_OK ? st : run_i8(a, workspace, workspace_bytes, reinterpret_cast<hipStream_t>(stream));
+}
+
+nm_status nm_glu_i8(const int8_t* x, int64_t t, int64_t k, int64_t ldx, const float* x_scale, const int8_t* w_gate,
+                    const float* gate_scale, const void* gate_meta, const int8_t* w_up, const float* up_scale,
+                    const void* up_meta, int64_t inter, int64_t ldw, nm_glu_act act, void* y, int64_t ldy,
+                    nm_ydtype y_dtype, void* workspace, int64_t workspace_bytes, uint32_t route,
+                    uint32_t* route_taken, void* stream) {
+  if (act != NM_GLU_SILU && act != NM_GLU_GELU_TANH) return NM_EINVAL;
+  nml::I8Args a{};
+  a.x = x; a.ldx = ldx; a.w = w_gate; a.w_up = w_up; a.ldw = ldw;
+  a.meta = static_cast<const uint8_t*>(gate_meta); a.up_meta = static_cast<const uint8_t*>(up_meta);
+  a.t = t; a.o = inter; a.k = k;
+  a.glu = 1;
+  a.epi = nml::I8Epi{x_scale, gate_scale, up_scale, nullptr, nullptr, y, ldy, (int)y_dtype, 0, (int)act};
+  a.route.flags = route;
+  a.route.taken = route_taken;
+  const nm_status st = check_i8(a, workspace, workspace_bytes);
+  return st != NM_OK ? st : run_i8(a, workspace, workspace_bytes, reinterpret_cast<hipStream_t>(stream));
+}
+
+int64_t nm_i8_workspace_size(int64_t t, int64_t o, int64_t k, int sparse, int glu, uint32_t route) {
+  (void)route;
+  if (t <= 0 || o <= 0 || k <= 0 || k > NM_I8_MAX_K || !span_ok(t, o)) return 0;
+  return nml::i8_few_part_bytes(t, o, k, sparse != 0, glu != 0);
+}
+
+}  // extern "C"

@@ -1,0 +1,59 @@
+// Device-side pieces shared by the int8 product kernels.
+#pragma once
+#include "i8_launch.h"
+#include "nm_device.h"
+
+namespace nmk {
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+// Sixteen readable zero bytes: where loads past the end of a row go.
+static __device__ const uint4 kZero16 = {0u, 0u, 0u, 0u};
+
+// Gate of a GLU in fp32.  silu: g / (1 + e^-g).  gelu: (1 + tanh z) / 2 = 1 / (1 + e^-2z), the
+// same function without the cancellation of 1 + tanh z for negative z (2 sqrt(2/pi) =
+// 1.5957691).  Where the exponential overflows the gate is its limit, -0 (also for g = -inf).
+// The exponent's rounding leaves the result |z| 2^-24 off, relative: at z = -20, where the
+// gate is 4e-8 of the largest, 1e-6.
+__device__ __forceinline__ float glu_gate(float g, int act) {
+  float z = g;
+  if (act == NM_GLU_GELU_TANH) z = 1.5957691216057308f * (g + 0.044715f * (g * g * g));
+  const float d = 1.0f + __expf(-z);
+  return d == __builtin_inff() ? -0.0f : g / d;
+}
+
+// fp32 to bf16, to nearest even; a NaN stays one.
+__device__ __forceinline__ uint16_t bf16_rne(float v) {
+  const uint32_t b = __float_as_uint(v);
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((b >> 16) | 0x40u);
+  return (uint16_t)((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
+}
+
+// The value of one output from its sums (s1: the second weight's, GLU).
+template <bool GLU>
+__device__ __forceinline__ float i8_value(const nml::I8Epi& e, int s0, int s1, float xs, float ws, float us, float rb,
+                                          float cs) {
+  const float v = ((float)s0 * xs) * ws;
+  if constexpr (GLU) return glu_gate(v, e.act) * (((float)s1 * xs) * us);
+  return v + rb * cs;
+}
+
+// One output, every address worked out (the few-token kernels and the reduction).
+template <bool GLU>
+__device__ __forceinline__ void i8_store(const nml::I8Epi& e, int s0, int s1, int64_t t, int64_t o) {
+  const float cs = !GLU && e.col_shift != nullptr ? e.col_shift[o] : 0.f;
+  const float rb = !GLU && e.row_shift != nullptr ? e.row_shift[t] : 1.f;
+  const float ws = e.w_scale[o], us = GLU ? e.up_scale[o] : 0.f;
+  const float xs = e.x_scale[t];
+  float v;
+  if (!GLU && e.col_shift == nullptr) v = ((float)s0 * xs) * ws;
+  else v = i8_value<GLU>(e, s0, s1, xs, ws, us, rb, cs);
+  if (e.bf16_out) {
+    static_cast<uint16_t*>(e.y)[t * e.ldy + o] = bf16_rne(v);
+  } else {
+    float* p = static_cast<float*>(e.y) + t * e.ldy + o;
+    *p = e.accumulate ? *p + v : v;
+  }
+}
+
+}  // namespace nmk
