@@ -46,9 +46,25 @@ nm_status check_i8(const nml::I8Args& a, const void* ws, int64_t ws_bytes) {
   return NM_OK;
 }
 
+enum class Kind { kFew, kMid, kLarge };
+
+// Streaming kernel up to 32 tokens; 256 x 256 tiles where they fill at least half the chip;
+// 128-row tiles with a split reduction between.
+Kind plan_i8(int64_t t, int64_t o, bool glu, uint32_t route) {
+  if (route & NM_ROUTE_FEW_STREAM) return Kind::kFew;
+  if (route & NM_ROUTE_FEW_TILE) return Kind::kMid;
+  if (route & NM_ROUTE_TILE_LDS) return Kind::kLarge;
+  if (t <= 32) return Kind::kFew;
+  const int64_t bo = glu ? 128 : 256;
+  return ((o + bo - 1) / bo) * ((t + 255) / 256) >= 128 ? Kind::kLarge : Kind::kMid;
+}
+
 nm_status run_i8(const nml::I8Args& a, void* ws, int64_t ws_bytes, hipStream_t s) {
   if (a.t == 0 || a.o == 0) return NM_OK;
-  return hip_status(nml::launch_i8_few(a, static_cast<int32_t*>(ws), ws_bytes, s));
+  const Kind kind = plan_i8(a.t, a.o, a.glu != 0, a.route.flags);
+  int32_t* part = static_cast<int32_t*>(ws);
+  if (kind == Kind::kFew || !nml::i8_tile_eligible(a)) return hip_status(nml::launch_i8_few(a, part, ws_bytes, s));
+  return hip_status(nml::launch_i8_tile(a, kind == Kind::kLarge, part, ws_bytes, s));
 }
 
 }  // namespace
@@ -121,9 +137,11 @@ nm_status nm_glu_i8(const int8_t* x, int64_t t, int64_t k, int64_t ldx, const fl
 }
 
 int64_t nm_i8_workspace_size(int64_t t, int64_t o, int64_t k, int sparse, int glu, uint32_t route) {
-  (void)route;
   if (t <= 0 || o <= 0 || k <= 0 || k > NM_I8_MAX_K || !span_ok(t, o)) return 0;
-  return nml::i8_few_part_bytes(t, o, k, sparse != 0, glu != 0);
+  const Kind kind = plan_i8(t, o, glu != 0, route);
+  if (kind == Kind::kLarge) return 0;
+  return kind == Kind::kFew ? nml::i8_few_part_bytes(t, o, k, sparse != 0, glu != 0)
+                            : nml::i8_mid_part_bytes(t, o, k, glu != 0);
 }
 
 }  // extern "C"

@@ -42,6 +42,12 @@ hipError_t launch_meta_step_block(const uint8_t* meta, int64_t o, int64_t kc, ui
 hipError_t launch_i8_few(const I8Args& a, int32_t* part, int64_t part_bytes, hipStream_t s);
 int64_t i8_few_part_bytes(int64_t t, int64_t o, int64_t k, bool sparse, bool glu);
 
+// Tile kernel: 256 x 256 tiles (large), or 128-row tiles with the reduction split across
+// workgroups where part holds i8_mid_part_bytes.
+bool i8_tile_eligible(const I8Args& a);
+int64_t i8_mid_part_bytes(int64_t t, int64_t o, int64_t k, bool glu);
+hipError_t launch_i8_tile(const I8Args& a, bool large, int32_t* part, int64_t part_bytes, hipStream_t s);
+
 // y from `splits` partial sums part[split][matrix][t][o4], o4 = o rounded up to 4
 hipError_t launch_i8_reduce(const int32_t* part, int64_t splits, bool glu, int64_t t, int64_t o, const I8Epi& e,
                             const Route& r, hipStream_t s);
