@@ -193,11 +193,23 @@ def _ld(t, default=0):
     return default
 
 
+_current_raw_stream = None      # () -> raw current stream of the current device
+
+
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    global _current_raw_stream
+    if _current_raw_stream is None:
+        import torch
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.current_stream()             # initialises the device
+        # building a Stream object costs 2.7 us a call, the raw handle 0.2 us (one-token calls take 6)
+        if raw is not None and device is not None:
+            _current_raw_stream = lambda: raw(device())  # noqa: E731
+        else:
+            _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_raw_stream()
 
 
 def _check(status: int, where: str):

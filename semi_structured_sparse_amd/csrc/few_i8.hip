@@ -30,12 +30,14 @@ struct FewCfg {
   static constexpr int NA = RW * (GLU ? 2 : 1);              // weight row blocks
   static constexpr int STEP = SP ? 128 : 64;                 // positions per matrix step
   static constexpr int REGS = NA * (SP ? 5 : 4) + TB * (SP ? 8 : 4);   // of one step's operands
-  static constexpr int FIT = (TB * NA >= 8 ? 200 : 88) / (2 * REGS);
+  // registers of a wave: 128 (16 waves a workgroup) or 256 (8); two batches are live
+  static constexpr bool BIG = TB >= 4;
+  static constexpr int FIT = ((BIG ? 256 : 128) - 24 - 4 * NA * TB - 2 * (NA * (SP ? 2 : 1) + TB)) / (2 * REGS);
   static constexpr int UNROLL = FIT < 1 ? 1 : FIT > 4 ? 4 : FIT;
 };
 
 template <int TB, int RW, bool SP, bool GLU>
-__global__ __launch_bounds__(TB * RW * (GLU ? 2 : 1) >= 8 ? 512 : 1024) void k_few_i8(
+__global__ __launch_bounds__(TB >= 4 ? 512 : 1024) void k_few_i8(
     const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w0, const int8_t* __restrict__ w1, int64_t ldw,
     const uint8_t* __restrict__ m0, const uint8_t* __restrict__ m1, int64_t T, int64_t O, int k, I8Epi epi,
     int32_t* __restrict__ part, int splits) {
@@ -80,21 +82,23 @@ __global__ __launch_bounds__(TB * RW * (GLU ? 2 : 1) >= 8 ? 512 : 1024) void k_f
   };
   const int wlen = SP ? k / 2 : k;        // weight bytes of a row
   const int64_t mstep = O * 16;
+  // whole: the step lies inside the part and the row on both sides; otherwise pieces past
+  // either come as zeros
   auto piece = [&](const int8_t* row, int off, bool in) {
     return *reinterpret_cast<const i32x4*>(in ? row + off : reinterpret_cast<const int8_t*>(&kZero16));
   };
-  // whole: the step lies inside the row on both sides
   auto load = [&](Batch& b, int u, int s, bool whole) {
     const int wo = s * 64, xo = s * C::STEP;
+    const bool in = whole || s < s1;
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
-      b.w[u][a] = piece(wrow[a], wo, whole || wo + 16 * fq < wlen);
-      if constexpr (SP) b.m[u][a] = *reinterpret_cast<const int*>(mrow[a] + s * mstep);
+      b.w[u][a] = piece(wrow[a], wo, whole || (in && wo + 16 * fq < wlen));
+      if constexpr (SP) b.m[u][a] = *reinterpret_cast<const int*>(mrow[a] + (in ? s : s1 - 1) * mstep);
     }
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
-      b.xl[u][j] = piece(xrow[j], xo, whole || xo + 16 * fq < k);
-      if constexpr (SP) b.xh[u][j] = piece(xrow[j], xo + 64, whole || xo + 64 + 16 * fq < k);
+      b.xl[u][j] = piece(xrow[j], xo, whole || (in && xo + 16 * fq < k));
+      if constexpr (SP) b.xh[u][j] = piece(xrow[j], xo + 64, whole || (in && xo + 64 + 16 * fq < k));
     }
   };
   auto mma = [&](const Batch& b, int u) {
@@ -113,40 +117,44 @@ __global__ __launch_bounds__(TB * RW * (GLU ? 2 : 1) >= 8 ? 512 : 1024) void k_f
       }
     }
   };
-  auto fetch = [&](Batch& b, int s) {
+  auto fetch = [&](Batch& b, int s, bool whole) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) load(b, u, s + u, true);
+    for (int u = 0; u < U; ++u) load(b, u, s + u, whole);
     __builtin_amdgcn_sched_barrier(0);   // the next batch's loads stay ahead of this one's products
   };
   auto consume = [&](const Batch& b) {
 #pragma unroll
     for (int u = 0; u < U; ++u) mma(b, u);
   };
-  const int whole = s1 < steps || k % C::STEP == 0 ? s1 : s1 - 1;   // steps inside the row
-  const int nb = whole > s0 ? (whole - s0) / U : 0;
+  // batches of U steps, one in flight ahead of the one multiplied; the last one may pass the
+  // part's or the row's end and is loaded with checks
+  const int nb = (s1 - s0 + U - 1) / U;
   if (nb > 0) {
     Batch b0, b1;
-    fetch(b0, s0);
     int b = 0;
-    while (b + 2 < nb) {
-      fetch(b1, s0 + (b + 1) * U);
-      consume(b0);
-      fetch(b0, s0 + (b + 2) * U);
-      consume(b1);
-      b += 2;
-    }
-    if (b + 2 == nb) {
-      fetch(b1, s0 + (b + 1) * U);
-      consume(b0);
-      consume(b1);
+    if (nb > 1) {
+      fetch(b0, s0, true);
+      for (; b + 3 < nb; b += 2) {
+        fetch(b1, s0 + (b + 1) * U, true);
+        consume(b0);
+        fetch(b0, s0 + (b + 2) * U, true);
+        consume(b1);
+      }
+      if (b + 3 == nb) {
+        fetch(b1, s0 + (b + 1) * U, true);
+        consume(b0);
+        fetch(b0, s0 + (b + 2) * U, false);
+        consume(b1);
+        consume(b0);
+      } else {
+        fetch(b1, s0 + (b + 1) * U, false);
+        consume(b0);
+        consume(b1);
+      }
     } else {
+      fetch(b0, s0, false);
       consume(b0);
     }
-  }
-  for (int s = s0 + nb * U; s < s1; ++s) {
-    Batch b;
-    load(b, 0, s, false);
-    mma(b, 0);
   }
 
   // the waves' partial tiles: red[wave][a][token][row]
@@ -203,21 +211,23 @@ __global__ __launch_bounds__(256) void k_i8_reduce(const int32_t* __restrict__ p
 }
 
 struct FewPlan {
-  int tb, waves;
+  int tb, rw, waves;
   int64_t splits;
 };
 
-// Waves and splits: the reduction in parts of at least 4 steps; row blocks times splits up to
-// about one workgroup per CU.
 FewPlan few_plan(int64_t t, int64_t o, int64_t k, bool sparse, bool glu) {
   FewPlan p;
   p.tb = t <= 16 ? 1 : t <= 32 ? 2 : 4;
   const int64_t steps = (k + (sparse ? 127 : 63)) / (sparse ? 128 : 64);
   const int mats = glu ? 2 : 1;
-  int64_t w = steps / 4;
-  const int most = p.tb * mats >= 8 ? 8 : 16;
-  p.waves = w >= 16 && most == 16 ? 16 : w >= 8 ? 8 : 4;
-  const int64_t blocks = ((o + 15) / 16) * ((t + 16 * p.tb - 1) / (16 * p.tb));
+  const int64_t gy = (t + 16 * p.tb - 1) / (16 * p.tb);
+  p.rw = p.tb > 2 || glu ? 1 : p.tb == 2 ? 2 : 4;
+  while (p.rw > 1 && ((o + 16 * p.rw - 1) / (16 * p.rw)) * gy < 200) p.rw /= 2;
+  const int64_t blocks = ((o + 16 * p.rw - 1) / (16 * p.rw)) * gy;
+  p.waves = blocks <= 128 ? 16 : blocks <= 512 ? 8 : 4;
+  const int most = p.tb == 4 || p.rw * mats * p.tb > 4 ? 8 : 16;   // 64 KiB of partial tiles
+  if (p.waves > most) p.waves = most;
+  while (p.waves > 4 && steps < 2 * p.waves) p.waves /= 2;
   int64_t s = blocks > 0 ? 256 / blocks : 1;
   const int64_t room = steps / (4 * p.waves);
   if (s > room) s = room;
@@ -225,9 +235,8 @@ FewPlan few_plan(int64_t t, int64_t o, int64_t k, bool sparse, bool glu) {
   return p;
 }
 
-template <int TB, bool SP, bool GLU>
+template <int TB, int RW, bool SP, bool GLU>
 hipError_t few_launch(const I8Args& a, const FewPlan& pl, int32_t* part, hipStream_t s) {
-  constexpr int RW = 1;
   using C = FewCfg<TB, RW, SP, GLU>;
   const int64_t nob = (a.o + 16 * RW - 1) / (16 * RW), gy = (a.t + 16 * TB - 1) / (16 * TB);
   if (nob * pl.splits > 0x7FFFFFFF || gy > 65535) return hipErrorInvalidConfiguration;
@@ -239,6 +248,17 @@ hipError_t few_launch(const I8Args& a, const FewPlan& pl, int32_t* part, hipStre
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.splits == 1) return e;
   return launch_i8_reduce(part, pl.splits, GLU, a.t, a.o, a.epi, a.route, s);
+}
+
+template <int TB, bool SP, bool GLU>
+hipError_t few_rows(const I8Args& a, const FewPlan& pl, int32_t* part, hipStream_t s) {
+  if constexpr (TB <= 2) {
+    if constexpr (!GLU) {
+      if (pl.rw == 4) return few_launch<TB, 4, SP, GLU>(a, pl, part, s);
+    }
+    if (pl.rw == 2) return few_launch<TB, 2, SP, GLU>(a, pl, part, s);
+  }
+  return few_launch<TB, 1, SP, GLU>(a, pl, part, s);
 }
 
 }  // namespace
@@ -268,10 +288,10 @@ hipError_t launch_i8_few(const I8Args& a, int32_t* part, int64_t part_bytes, hip
   if (part == nullptr || part_bytes < i8_few_part_bytes(a.t, a.o, a.k, sp, glu)) p.splits = 1;
 #define NM_FEW(TBV)                                                       \
   if (p.tb == TBV) {                                                      \
-    if (sp && glu) return few_launch<TBV, true, true>(a, p, part, s);     \
-    if (sp) return few_launch<TBV, true, false>(a, p, part, s);           \
-    if (glu) return few_launch<TBV, false, true>(a, p, part, s);          \
-    return few_launch<TBV, false, false>(a, p, part, s);                  \
+    if (sp && glu) return few_rows<TBV, true, true>(a, p, part, s);     \
+    if (sp) return few_rows<TBV, true, false>(a, p, part, s);           \
+    if (glu) return few_rows<TBV, false, true>(a, p, part, s);          \
+    return few_rows<TBV, false, false>(a, p, part, s);                  \
   }
   NM_FEW(1) NM_FEW(2) NM_FEW(4)
 #undef NM_FEW
