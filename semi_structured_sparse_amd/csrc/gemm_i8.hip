@@ -56,6 +56,209 @@ __device__ __forceinline__ void k_loop2(int n, unsigned char* a0, unsigned char*
   }
 }
 
+// Two fp32 values as packed bf16, to nearest even.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
+// The output factors of a tile in LDS (requested before the K-loop: loaded after it they cost
+// 4 us a tile): w_scale, then up_scale (GLU) or col_shift of BO outputs, past O the last one.
+// Waves 0 .. 2 BO / 64 - 1 load 64 each.
+template <int BO, bool GLU, int NW>
+__device__ __forceinline__ void load_factors(const I8Epi& epi, int64_t o0, int64_t O, int wave, int lane, float* sw) {
+  constexpr int PER = BO / 64;
+#pragma unroll
+  for (int q = 0; q < (2 * PER + NW - 1) / NW; ++q) {
+    const int g = wave + q * NW;
+    if (g >= 2 * PER) break;
+    const float* src = g < PER ? epi.w_scale : GLU ? epi.up_scale : epi.col_shift;
+    if (src == nullptr) break;
+    int64_t o = o0 + (g % PER) * 64 + lane;
+    o = o < O ? o : O - 1;
+    __builtin_amdgcn_global_load_lds(src + o, (lds_void*)(sw + g * 64), 4, 0, 0);
+  }
+}
+
+// What a wave does with its finished sums: FI x FJ blocks of 16 x 16, lane (fr, fq) = (lane & 15,
+// lane >> 4) holding rows 4 fq + [0, 4) of each block's row range for token fr.  ob_w, tb_w: the
+// wave's first output and token (ow: that output in the tile).  With a split reduction the sums go to part; otherwise each
+// block column's outputs are scaled, turned through the wave's own TURN bytes of LDS at
+// `mine` (a row of 64 outputs per token, 16-byte piece c of row r at c ^ r) and stored as
+// whole row pieces: 128 bytes of bf16 or 256 of fp32.  TURN = 0, or rows that are not
+// 16-byte aligned: element by element.
+template <int FI, int FJ, bool GLU, int TURN>
+__device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Epi& epi, int32_t* __restrict__ part,
+                                          int kpart, int64_t T, int64_t O, int64_t ob_w, int64_t tb_w, int lane,
+                                          unsigned char* mine, const float* sw, int BO, int ow) {
+  const int fr = lane & 15, fq = lane >> 4;
+  constexpr int NO = GLU ? FI / 2 : FI;         // output blocks of 16
+  const int64_t ob0 = ob_w + 4 * fq, tb0 = tb_w + fr;
+  if (part != nullptr) {
+    const int64_t o4 = (O + 3) / 4 * 4;
+#pragma unroll
+    for (int i = 0; i < NO; ++i) {
+      const int64_t ob = ob0 + 16 * i;
+      if (ob >= O) continue;
+#pragma unroll
+      for (int j = 0; j < FJ; ++j) {
+        const int64_t t = tb0 + 16 * j;
+        if (t >= T) continue;
+        int32_t* pp = part + ((int64_t)kpart * (GLU ? 2 : 1) * T + t) * o4 + ob;
+        *reinterpret_cast<i32x4*>(pp) = acc[GLU ? 2 * i : i][j];
+        if constexpr (GLU) *reinterpret_cast<i32x4*>(pp + T * o4) = acc[2 * i + 1][j];
+      }
+    }
+    return;
+  }
+  // the tokens' factors first: a load per block column would stall each of them
+  float xs[FJ], rb[FJ];
+#pragma unroll
+  for (int j = 0; j < FJ; ++j) {
+    const int64_t t = tb0 + 16 * j < T ? tb0 + 16 * j : T - 1;
+    xs[j] = epi.x_scale[t];
+    rb[j] = !GLU && epi.row_shift != nullptr ? epi.row_shift[t] : 1.f;
+  }
+  const bool shifted = !GLU && epi.col_shift != nullptr;
+  struct Scales {
+    float w[4], u[4], c[4];
+  };
+  auto scales = [&](int i) {   // of the lane's four outputs in block i
+    Scales sc;
+    const int at = ow + 16 * i + 4 * fq;   // in the tile
+    const f32x4 w = *reinterpret_cast<const f32x4*>(sw + at);
+    const f32x4 e = GLU || shifted ? *reinterpret_cast<const f32x4*>(sw + BO + at) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      sc.w[r] = w[r];
+      sc.u[r] = e[r];
+      sc.c[r] = e[r];
+    }
+    return sc;
+  };
+  auto value = [&](const Scales& sc, int i, int j, int r) {
+    const int s0 = acc[GLU ? 2 * i : i][j][r], s1 = GLU ? acc[GLU ? 2 * i + 1 : i][j][r] : 0;
+    if (!GLU && !shifted) return ((float)s0 * xs[j]) * sc.w[r];
+    return i8_value<GLU>(epi, s0, s1, xs[j], sc.w[r], sc.u[r], rb[j], sc.c[r]);
+  };
+  if constexpr (TURN > 0) {
+    static_assert(NO % 4 == 0 && TURN >= 4096, "rows of 64 outputs");
+    constexpr int JB = TURN >= 8192 && FJ % 2 == 0 ? 2 : 1;   // block columns turned at a time
+    if (epi.bf16_out && epi.ldy % 8 == 0) {
+#pragma unroll
+      for (int h = 0; h < NO / 4; ++h) {
+        const int64_t oh = ob_w + 64 * h;
+        Scales sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] = scales(4 * h + i);
+#pragma unroll
+        for (int j0 = 0; j0 < FJ; j0 += JB) {
+#pragma unroll
+          for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float v[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] = value(sc[i], 4 * h + i, j0 + jj, r);
+              *reinterpret_cast<uint2*>(mine + jj * 2048 + fr * 128 + 16 * ((2 * i + (fq >> 1)) ^ (fr & 7)) + 8 * (fq & 1)) =
+                  make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+            }
+          __builtin_amdgcn_wave_barrier();
+          uint4 d[2 * JB];
+#pragma unroll
+          for (int p = 0; p < 2 * JB; ++p) {
+            const int row = 8 * p + (lane >> 3);
+            d[p] = *reinterpret_cast<const uint4*>(mine + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
+          }
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int p = 0; p < 2 * JB; ++p) {
+            const int64_t t = tb_w + 16 * j0 + 8 * p + (lane >> 3), o = oh + 8 * (lane & 7);
+            if (t >= T || o >= O) continue;
+            uint16_t* yp = static_cast<uint16_t*>(epi.y) + t * epi.ldy + o;
+            if (o + 8 <= O) {
+              *reinterpret_cast<uint4*>(yp) = d[p];
+            } else {
+              const uint32_t e[4] = {d[p].x, d[p].y, d[p].z, d[p].w};
+#pragma unroll
+              for (int r = 0; r < 8; ++r)
+                if (o + r < O) yp[r] = (uint16_t)(e[r >> 1] >> (16 * (r & 1)));
+            }
+          }
+        }
+      }
+      return;
+    }
+    if (!epi.bf16_out && epi.ldy % 4 == 0) {
+#pragma unroll
+      for (int h = 0; h < NO / 4; ++h) {
+        const int64_t oh = ob_w + 64 * h;
+        Scales sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] = scales(4 * h + i);
+#pragma unroll
+        for (int j0 = 0; j0 < FJ; j0 += JB) {
+#pragma unroll
+          for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f32x4 v;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] = value(sc[i], 4 * h + i, j0 + jj, r);
+              *reinterpret_cast<f32x4*>(mine + jj * 4096 + fr * 256 + 16 * ((4 * i + fq) ^ fr)) = v;
+            }
+          __builtin_amdgcn_wave_barrier();
+          f32x4 d[4 * JB];
+#pragma unroll
+          for (int p = 0; p < 4 * JB; ++p) {
+            const int row = 4 * p + (lane >> 4);
+            d[p] = *reinterpret_cast<const f32x4*>(mine + row * 256 + 16 * ((lane & 15) ^ (row & 15)));
+          }
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int p = 0; p < 4 * JB; ++p) {
+            const int64_t t = tb_w + 16 * j0 + 4 * p + (lane >> 4), o = oh + 4 * (lane & 15);
+            if (t >= T || o >= O) continue;
+            float* yp = static_cast<float*>(epi.y) + t * epi.ldy + o;
+            if (o + 4 <= O) {
+              if (epi.accumulate) d[p] += *reinterpret_cast<const f32x4*>(yp);
+              *reinterpret_cast<f32x4*>(yp) = d[p];
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (o + r < O) yp[r] = epi.accumulate ? yp[r] + d[p][r] : d[p][r];
+            }
+          }
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NO; ++i) {
+    const Scales sc = scales(i);
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) {
+      const int64_t t = tb0 + 16 * j;
+      if (t >= T) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t o = ob0 + 16 * i + r;
+        if (o >= O) continue;
+        const float v = value(sc, i, j, r);
+        if (epi.bf16_out) {
+          static_cast<uint16_t*>(epi.y)[t * epi.ldy + o] = bf16_rne(v);
+        } else {
+          float* p = static_cast<float*>(epi.y) + t * epi.ldy + o;
+          *p = epi.accumulate ? *p + v : v;
+        }
+      }
+    }
+  }
+}
+
 // BM x BN: weight rows by tokens of a tile (GLU: BM / 2 outputs); WM x WN waves; NST stages.
 template <int BM, int BN, int WM, int WN, bool SP, bool GLU, int NST>
 __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
@@ -77,19 +280,22 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
   __shared__ __align__(16) unsigned char sA0[A_BYTES], sB0[B_BYTES];
   __shared__ __align__(16) unsigned char sA1[A_BYTES], sB1[B_BYTES];
   __shared__ __align__(16) unsigned char sA2[A2], sB2[B2];
+  __shared__ __align__(16) float sw[2 * (BO < 64 ? 64 : BO)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wmi = wave % WM, wni = wave / WM;
   const int fr = lane & 15, fq = lane >> 4;
 
   const int ntiles = tiles_m * tiles_n;
-  const int kpart = blockIdx.x / ntiles;
+  const int kpart = __builtin_amdgcn_readfirstlane(blockIdx.x / ntiles);
   int lin = blockIdx.x - kpart * ntiles;
   if ((ntiles & 7) == 0 && gridDim.x == (unsigned)ntiles) lin = (blockIdx.x & 7) * (ntiles >> 3) + (blockIdx.x >> 3);
   const int band = lin / (group * tiles_n);
   const int band_w = min(group, tiles_m - band * group);
   const int inband = lin - band * group * tiles_n;
-  const int tile_m = band * group + inband % band_w, tile_n = inband / band_w;
+  // wave-uniform (the division leaves them in vector registers; descriptors need scalars)
+  const int tile_m = __builtin_amdgcn_readfirstlane(band * group + inband % band_w);
+  const int tile_n = __builtin_amdgcn_readfirstlane(inband / band_w);
   const int64_t o0 = (int64_t)tile_m * BO, t0 = (int64_t)tile_n * BN;
   const int orows = (int)(O - o0 < BO ? O - o0 : BO), trows = (int)(T - t0 < BN ? T - t0 : BN);
 
@@ -134,6 +340,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
     moff = (uint32_t)(o * 16);
     mbase = m0 + o0 * 16;
   }
+
+  if (part == nullptr) load_factors<BO, GLU, NW>(epi, o0, O, wave, lane, sw);
 
   i32x4 acc[FI][FJ];
 #pragma unroll
@@ -246,144 +454,345 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
     }
   }
 
-  // lane: outputs ob + [0, 4) of each block row, token tb of each block column
-  constexpr int NO = GLU ? FI / 2 : FI;         // output blocks of 16
-  const int64_t ob0 = o0 + (GLU ? wmi * SM / 2 : wmi * SM) + 4 * fq;
-  const int64_t tb0 = t0 + wni * SN + fr;
-  if (part != nullptr) {
-    const int64_t o4 = (O + 3) / 4 * 4;
+  constexpr int TURN = (GLU ? FI / 2 : FI) % 4 != 0 ? 0 : B_BYTES >= NW * 4096 ? 4096 : 0;
+  const int ow = GLU ? wmi * SM / 2 : wmi * SM;
+  i8_finish<FI, FJ, GLU, TURN>(acc, epi, part, kpart, T, O, o0 + ow, t0 + wni * SN, lane, sB0 + wave * TURN, sw, BO, ow);
+}
+
+// ----------------------------------------------------------- the large 2:4 products ---
+
+// acc += a b on the accumulator half of the register file.  Written out because the compiler,
+// with all 256 registers of that half taken by sums, moved or spilled a hundred of them per
+// step (658 us against 277 at 8192 x 4096 x 14336).  It does not see this as a matrix
+// instruction, so the waits it would insert are here: s_nop 1 ahead (an operand just written
+// by a vector instruction), mma_done() before the sums are read.
+__device__ __forceinline__ void smma_acc(i32x16& c, i32x4 a, i32x8 b, int idx) {
+  asm volatile("s_nop 1\n\tv_smfmac_i32_32x32x64_i8 %0, %1, %2, %3" : "+a"(c) : "v"(a), "v"(b), "v"(idx));
+}
+template <int N>
+__device__ __forceinline__ void mma_done(i32x16 (&acc)[N][N]) {
+  asm volatile("s_nop 15\n\ts_nop 15");
 #pragma unroll
-    for (int i = 0; i < NO; ++i) {
-      const int64_t ob = ob0 + 16 * i;
-      if (ob >= O) continue;
+  for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < FJ; ++j) {
-        const int64_t t = tb0 + 16 * j;
-        if (t >= T) continue;
-        int32_t* pp = part + ((int64_t)kpart * (GLU ? 2 : 1) * T + t) * o4 + ob;
-        *reinterpret_cast<i32x4*>(pp) = acc[GLU ? 2 * i : i][j];
-        if constexpr (GLU) *reinterpret_cast<i32x4*>(pp + T * o4) = acc[2 * i + 1][j];
-      }
-    }
-    return;
+    for (int j = 0; j < N; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+// one sum, read when it is used (read together they would need 256 more registers)
+__device__ __forceinline__ int acc_read(int a) {
+  int v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+  return v;
+}
+
+// The finished sums of a wave's 4 x 4 blocks of 32 x 32: lane (c, h) = (lane & 31, lane >> 5)
+// holds, in register v, row 8 (v / 4) + 4 h + v % 4 of token c.  GLU: the rows of a block are 16
+// gate rows and the 16 up rows of the same outputs, registers v and v + 8.  As i8_finish: rows
+// of 64 outputs and 32 tokens are turned in the wave's own 8 KiB of LDS and stored whole.
+template <bool GLU>
+__device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I8Epi& epi, int64_t T, int64_t O,
+                                              int64_t ob_w, int64_t tb_w, int lane, unsigned char* mine,
+                                              const float* sw, int ow) {
+  const int c = lane & 31, h = lane >> 5;
+  constexpr int BO = GLU ? 128 : 256;
+  constexpr int NB = GLU ? 4 : 2;      // blocks of 64 outputs
+  constexpr int NG = GLU ? 2 : 4;      // groups of 4 outputs of a lane per block: outputs 8 g + 4 h + [0, 4)
+  constexpr int NH = GLU ? 1 : 2;      // 64-output parts of the wave
+  const bool shifted = !GLU && epi.col_shift != nullptr;
+  float xs[4], rb[4];                  // the tokens' factors first: a load per block would stall each
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t t = tb_w + 32 * j + c < T ? tb_w + 32 * j + c : T - 1;
+    xs[j] = epi.x_scale[t];
+    rb[j] = !GLU && epi.row_shift != nullptr ? epi.row_shift[t] : 1.f;
   }
-  const int esz = epi.bf16_out ? 2 : 4;
-  struct Scales {
-    float w[4], u[4], c[4];
-  };
-  auto scales = [&](int i) {   // of the lane's four outputs in block i
-    Scales sc;
+  const bool rows16 = epi.bf16_out ? epi.ldy % 8 == 0 : epi.ldy % 4 == 0;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t o = ob0 + 16 * i + r < O ? ob0 + 16 * i + r : O - 1;
-      sc.w[r] = epi.w_scale[o];
-      sc.u[r] = GLU ? epi.up_scale[o] : 0.f;
-      sc.c[r] = !GLU && epi.col_shift != nullptr ? epi.col_shift[o] : 0.f;
-    }
-    return sc;
-  };
-  auto value = [&](const Scales& sc, int i, int j, int r, float xs, float rb) {
-    const int s0 = acc[GLU ? 2 * i : i][j][r], s1 = GLU ? acc[GLU ? 2 * i + 1 : i][j][r] : 0;
-    if (!GLU && epi.col_shift == nullptr) return ((float)s0 * xs) * sc.w[r];
-    return i8_value<GLU>(epi, s0, s1, xs, sc.w[r], sc.u[r], rb, sc.c[r]);
-  };
-  constexpr bool TURN = B_BYTES >= NW * 4096 && NO % 4 == 0;
-  // pieces of 16 bytes of an output row: whole rows of 64 outputs, aligned
-  const bool vec = TURN && (epi.ldy * esz) % 16 == 0;
-  if (TURN && vec) {
-    // 64 outputs x 16 tokens at a time: fp32 rows of 256 bytes in the wave's 4 KiB, piece c of
-    // row r at c ^ r
-    unsigned char* const mine = sB0 + wave * 4096;
+  for (int hh = 0; hh < NH; ++hh) {
+    const int64_t oh = ob_w + 64 * hh;
+    f32x4 ws[NB][NG], es[NB][NG];   // w_scale, and up_scale (GLU) or col_shift
 #pragma unroll
-    for (int h = 0; h < NO / 4; ++h) {
-      const int64_t oh = o0 + (GLU ? wmi * SM / 2 : wmi * SM) + 64 * h;
-      Scales sc[4];
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i] = scales(4 * h + i);
+      for (int g = 0; g < NG; ++g) {
+        const float* at = sw + ow + 64 * hh + (GLU ? 16 : 32) * b + 8 * g + 4 * h;
+        ws[b][g] = *reinterpret_cast<const f32x4*>(at);
+        es[b][g] = GLU || shifted ? *reinterpret_cast<const f32x4*>(at + BO) : f32x4{0.f, 0.f, 0.f, 0.f};
+      }
 #pragma unroll
-      for (int j = 0; j < FJ; ++j) {
-        const int64_t t = tb0 + 16 * j, tc = t < T ? t : T - 1;
-        const float xs = epi.x_scale[tc];
-        const float rb = !GLU && epi.row_shift != nullptr ? epi.row_shift[tc] : 1.f;
+    for (int j = 0; j < 4; ++j) {
+      float v[NB][NG][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f32x4 v;
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = value(sc[i], 4 * h + i, j, r, xs, rb);
-          *reinterpret_cast<f32x4*>(mine + fr * 256 + 16 * ((4 * i + fq) ^ fr)) = v;
-        }
-        __builtin_amdgcn_wave_barrier();
-        if (epi.bf16_out) {
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int row = 8 * p + (lane >> 3), c = 2 * (lane & 7);
-            const f32x4 u = *reinterpret_cast<const f32x4*>(mine + row * 256 + 16 * (c ^ row));
-            const f32x4 v = *reinterpret_cast<const f32x4*>(mine + row * 256 + 16 * ((c + 1) ^ row));
-            const int64_t tt = t0 + wni * SN + 16 * j + row, o = oh + 4 * c;
-            if (tt >= T || o >= O) continue;
-            uint16_t* yp = static_cast<uint16_t*>(epi.y) + tt * epi.ldy + o;
-            uint16_t h8[8];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              h8[r] = bf16_rne(u[r]);
-              h8[4 + r] = bf16_rne(v[r]);
-            }
-            if (o + 8 <= O) {
-              *reinterpret_cast<uint4*>(yp) =
-                  make_uint4(h8[0] | (uint32_t)h8[1] << 16, h8[2] | (uint32_t)h8[3] << 16, h8[4] | (uint32_t)h8[5] << 16,
-                             h8[6] | (uint32_t)h8[7] << 16);
+          for (int r = 0; r < 4; ++r) {
+            const i32x16& blk = acc[GLU ? b : 2 * hh + b][j];
+            const int s0 = acc_read(blk[4 * g + r]);
+            if constexpr (GLU) {
+              const int s1 = acc_read(blk[8 + 4 * g + r]);
+              v[b][g][r] = i8_value<true>(epi, s0, s1, xs[j], ws[b][g][r], es[b][g][r], 0.f, 0.f);
             } else {
-#pragma unroll
-              for (int r = 0; r < 8; ++r)
-                if (o + r < O) yp[r] = h8[r];
+              v[b][g][r] = ((float)s0 * xs[j]) * ws[b][g][r];
             }
           }
-        } else {
+      if (shifted) {
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const int row = 4 * p + (lane >> 4), c = lane & 15;
-            f32x4 v = *reinterpret_cast<const f32x4*>(mine + row * 256 + 16 * (c ^ row));
-            const int64_t tt = t0 + wni * SN + 16 * j + row, o = oh + 4 * c;
-            if (tt >= T || o >= O) continue;
-            float* yp = static_cast<float*>(epi.y) + tt * epi.ldy + o;
-            if (o + 4 <= O) {
-              if (epi.accumulate) v += *reinterpret_cast<const f32x4*>(yp);
-              *reinterpret_cast<f32x4*>(yp) = v;
-            } else {
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (o + r < O) yp[r] = epi.accumulate ? yp[r] + v[r] : v[r];
-            }
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[b][g][r] += rb[j] * es[b][g][r];
+      }
+      const int64_t tj = tb_w + 32 * j;
+      if (epi.bf16_out) {
+        // rows of 128 bytes: 8-byte halves of piece p of token c at p ^ ((c >> 1) & 7)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const int p = (GLU ? 2 : 4) * b + g;
+            *reinterpret_cast<uint2*>(mine + c * 128 + 16 * (p ^ ((c >> 1) & 7)) + 8 * h) =
+                make_uint2(bf16x2(v[b][g][0], v[b][g][1]), bf16x2(v[b][g][2], v[b][g][3]));
           }
+        __builtin_amdgcn_wave_barrier();
+        uint4 d[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int row = 8 * p + (lane >> 3);
+          d[p] = *reinterpret_cast<const uint4*>(mine + row * 128 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
         }
         __builtin_amdgcn_wave_barrier();
-      }
-    }
-    return;
-  }
 #pragma unroll
-  for (int i = 0; i < NO; ++i) {
-    const Scales sc = scales(i);
+        for (int p = 0; p < 4; ++p) {
+          const int64_t t = tj + 8 * p + (lane >> 3), o = oh + 8 * (lane & 7);
+          if (t >= T || o >= O) continue;
+          uint16_t* yp = static_cast<uint16_t*>(epi.y) + t * epi.ldy + o;
+          if (rows16 && o + 8 <= O) {
+            *reinterpret_cast<uint4*>(yp) = d[p];
+          } else {
+            const uint32_t e[4] = {d[p].x, d[p].y, d[p].z, d[p].w};
 #pragma unroll
-    for (int j = 0; j < FJ; ++j) {
-      const int64_t t = tb0 + 16 * j;
-      if (t >= T) continue;
-      const float xs = epi.x_scale[t];
-      const float rb = !GLU && epi.row_shift != nullptr ? epi.row_shift[t] : 1.f;
+            for (int r = 0; r < 8; ++r)
+              if (o + r < O) yp[r] = (uint16_t)(e[r >> 1] >> (16 * (r & 1)));
+          }
+        }
+      } else {
+        // rows of 256 bytes: piece p of token c at p ^ (c & 15)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t o = ob0 + 16 * i + r;
-        if (o >= O) continue;
-        const float v = value(sc, i, j, r, xs, rb);
-        if (epi.bf16_out) {
-          static_cast<uint16_t*>(epi.y)[t * epi.ldy + o] = bf16_rne(v);
-        } else {
-          float* p = static_cast<float*>(epi.y) + t * epi.ldy + o;
-          *p = epi.accumulate ? *p + v : v;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const int p = (GLU ? 4 : 8) * b + 2 * g + h;
+            *reinterpret_cast<f32x4*>(mine + c * 256 + 16 * (p ^ (c & 15))) =
+                f32x4{v[b][g][0], v[b][g][1], v[b][g][2], v[b][g][3]};
+          }
+        __builtin_amdgcn_wave_barrier();
+        f32x4 d[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int row = 4 * p + (lane >> 4);
+          d[p] = *reinterpret_cast<const f32x4*>(mine + row * 256 + 16 * ((lane & 15) ^ (row & 15)));
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int64_t t = tj + 4 * p + (lane >> 4), o = oh + 4 * (lane & 15);
+          if (t >= T || o >= O) continue;
+          float* yp = static_cast<float*>(epi.y) + t * epi.ldy + o;
+          if (rows16 && o + 4 <= O) {
+            if (epi.accumulate) d[p] += *reinterpret_cast<const f32x4*>(yp);
+            *reinterpret_cast<f32x4*>(yp) = d[p];
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (o + r < O) yp[r] = epi.accumulate ? yp[r] + d[p][r] : d[p][r];
+          }
         }
       }
     }
   }
+}
+
+// 256 x 256 tiles of 2:4 products by 4 waves of 128 x 128 (one per SIMD, 256 sums a lane).  A wave
+// reads 256 rows of LDS for 128 x 128 outputs, so LDS, which bounds the 8-wave form (twice the
+// matrix rate of dense products on the same X bytes), moves three quarters as much: 8192 x
+// 4096 x 14336 311 -> 271 us, GLU 4096 x 14336 x 4096 313 -> 303 us.  (Dense products gain
+// nothing: 384 us with 8 waves, 394-417 with 4.)  Nothing but the wave itself hides a latency,
+// so operands are read two phases of 16 matrix instructions ahead, a read or a request
+// between two of them:
+//  * v_smfmac_i32_32x32x64_i8: lane (c, h) = (lane & 31, lane >> 5) holds the 16 kept codes of
+//    row c at positions [32 h, + 32) of a 64-position phase with their 32 bits of positions,
+//    and of X the bytes [16 h, + 16) and [32 + 16 h, + 16).
+//  * A step of 128 positions is two phases; 3 stages of 52 KiB.  When a step begins, its operands
+//    are in registers and the next step's have landed: one wait, one barrier, and the stage
+//    takes the requests of the step after the next two.
+// What bounds it: with no requests and real data 211 us (the matrix pipe alone 165 us: power
+// holds its clock down, the same loop on constant operands takes 132), the requests' LDS
+// writes and L2 latency 60 us, epilogue 30 us.
+template <bool GLU>
+__global__ __launch_bounds__(256) void k_i8_big(
+    const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w0, const int8_t* __restrict__ w1, int64_t ldw,
+    const uint8_t* __restrict__ m0, const uint8_t* __restrict__ m1, int64_t T, int64_t O, int k, I8Epi epi, int tiles_m,
+    int tiles_n, int group) {
+  constexpr int BM = 256, BN = 256, NW = 4;
+  constexpr int BO = GLU ? BM / 2 : BM;
+  constexpr int V_BYTES = BM * 64, A_BYTES = V_BYTES + BM * 16, B_BYTES = BN * 128;   // codes, positions; X
+  constexpr int NA = BM / 16 / NW, NB = BN / 8 / NW, NL = NA + NB + 1;   // loads of a wave per step
+  __shared__ __align__(16) unsigned char s0[A_BYTES + B_BYTES], s1[A_BYTES + B_BYTES], s2[A_BYTES + B_BYTES];
+  __shared__ __align__(16) float sw[2 * BO];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wmi = wave & 1, wni = wave >> 1;
+  const int c = lane & 31, h = lane >> 5;
+
+  const int ntiles = tiles_m * tiles_n;
+  int lin = blockIdx.x;
+  if ((ntiles & 7) == 0) lin = (blockIdx.x & 7) * (ntiles >> 3) + (blockIdx.x >> 3);
+  const int band = lin / (group * tiles_n);
+  const int band_w = min(group, tiles_m - band * group);
+  const int inband = lin - band * group * tiles_n;
+  // wave-uniform (the division leaves them in vector registers; descriptors need scalars)
+  const int tile_m = __builtin_amdgcn_readfirstlane(band * group + inband % band_w);
+  const int tile_n = __builtin_amdgcn_readfirstlane(inband / band_w);
+  const int64_t o0 = (int64_t)tile_m * BO, t0 = (int64_t)tile_n * BN;
+  const int orows = (int)(O - o0 < BO ? O - o0 : BO), trows = (int)(T - t0 < BN ? T - t0 : BN);
+  const int n = (k + 127) / 128;   // steps, >= 1
+
+  // descriptors and offsets as in k_i8_tile; a wave's weight loads are all of one matrix
+  const bool up = GLU && (wave & 1);
+  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x + t0 * ldx, (uint32_t)(trows * ldx));
+  const __amdgpu_buffer_rsrc_t rw = rsrc_of((up ? w1 : w0) + o0 * ldw, (uint32_t)(orows * ldw));
+  uint32_t aoff[NA], boff[NB];
+  uint32_t amask = 0, bmask = 0;   // kPast where the lane's piece of the last step starts past the row
+  const int last = (n - 1) * 128;
+#pragma unroll
+  for (int q = 0; q < NA; ++q) {
+    const int r = (wave + q * NW) * 16 + (lane >> 2);
+    const int p = swz4(r, lane & 3);
+    int o = GLU ? (r >> 5) * 16 + (r & 15) : r;
+    o = o < orows ? o : orows - 1;
+    aoff[q] = (uint32_t)(o * (int)ldw + 16 * p);
+    if (q == 0) amask = last / 2 + 16 * p >= k / 2 ? kPast : 0u;
+  }
+#pragma unroll
+  for (int q = 0; q < NB; ++q) {
+    const int r = (wave + q * NW) * 8 + (lane >> 3);
+    const int p = swz8(r, lane & 7);
+    const int t = r < trows ? r : trows - 1;
+    boff[q] = (uint32_t)(t * (int)ldx + 16 * p);
+    if (q == 0) bmask = last + 16 * p >= k ? kPast : 0u;
+  }
+  const uint8_t* mlane;   // the lane's positions in step block 0
+  const int64_t mstep = O * 16;
+  {
+    const int r = wave * 64 + lane;
+    int o = GLU ? (r >> 5) * 16 + (r & 15) : r;
+    o = o < orows ? o : orows - 1;
+    mlane = (GLU && ((lane >> 4) & 1) ? m1 : m0) + (o0 + o) * 16;
+  }
+  int ls = 0;   // the step being requested; past the last one the last again (no one reads it)
+  auto begin_loads = [&](int s) {
+    ls = s < n ? s : n - 1;
+    const uint32_t am = ls == n - 1 ? amask : 0u, bm = ls == n - 1 ? bmask : 0u;
+#pragma unroll
+    for (int q = 0; q < NA; ++q) aoff[q] |= am;
+#pragma unroll
+    for (int q = 0; q < NB; ++q) boff[q] |= bm;
+  };
+  auto load = [&](unsigned char* st, int q) {   // load q of step ls into stage st
+    if (q < NA) {
+      b2lds16(rw, st + (wave + q * NW) * 1024, aoff[q], (uint32_t)(ls * 64));
+    } else if (q < NA + NB) {
+      const int p = q - NA;
+      b2lds16(rx, st + A_BYTES + (wave + p * NW) * 1024, boff[p], (uint32_t)(ls * 128));
+    } else {
+      __builtin_amdgcn_global_load_lds(mlane + ls * mstep, (lds_void*)(st + V_BYTES + wave * 1024), 16, 0, 0);
+    }
+  };
+  auto bar = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto lds4 = [](const unsigned char* p) { return *reinterpret_cast<const i32x4*>(p); };
+  // fragment addresses: rows 32 i + c of the wave's 128, whose swizzle does not depend on i
+  const int ab = (wmi * 128 + c) * 64, bb = A_BYTES + (wni * 128 + c) * 128;
+  const int ms = V_BYTES + (wmi * 128 + c) * 16 + 4 * h;
+  int apos[2], bpos[4];   // pieces 2 e + h of a weight row, of a token row
+#pragma unroll
+  for (int e = 0; e < 2; ++e) apos[e] = ab + 16 * swz4(c, 2 * e + h);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) bpos[e] = bb + 16 * swz8(c, 2 * e + h);
+
+  load_factors<BO, GLU, NW>(epi, o0, O, wave, lane, sw);
+
+  i32x16 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+
+  struct Frag {
+    i32x4 a[4];
+    i32x8 b[4];
+    int idx[4];
+  };
+  auto read = [&](Frag& f, const unsigned char* st, int ks, int e) {   // read e of 12 (two for X)
+    if (e < 4) f.a[e] = lds4(st + apos[ks] + e * 2048);
+    else if (e < 8) f.idx[e - 4] = *reinterpret_cast<const int*>(st + ms + 8 * ks + (e - 4) * 512);
+    else f.b[e - 8] = __builtin_shufflevector(lds4(st + bpos[2 * ks] + (e - 8) * 4096),
+                                              lds4(st + bpos[2 * ks + 1] + (e - 8) * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto phase = [&](const Frag& f, Frag& fn, const unsigned char* rd, int ks, bool LOAD, unsigned char* wr) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int j = e >> 2, i = e & 3;
+      smma_acc(acc[i][j], f.a[i], f.b[j], f.idx[i]);
+      if (e < 12) read(fn, rd, ks, e < 8 ? ((e & 1) ? 4 + e / 2 : e / 2) : e);
+      if (LOAD && e < NL) load(wr, e);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  static_assert(NL <= 16, "a load per product");
+  Frag f0, f1, f2;   // part p of step s is the (2 s + p) % 3rd
+  begin_loads(0);
+#pragma unroll
+  for (int q = 0; q < NL; ++q) load(s0, q);
+  begin_loads(1);
+#pragma unroll
+  for (int q = 0; q < NL; ++q) load(s1, q);
+  begin_loads(2);
+#pragma unroll
+  for (int q = 0; q < NL; ++q) load(s2, q);
+  __builtin_amdgcn_s_waitcnt(vm_wait(2 * NL));
+  bar();
+#pragma unroll
+  for (int e = 0; e < 12; ++e) read(f0, s0, 0, e);
+#pragma unroll
+  for (int e = 0; e < 12; ++e) read(f1, s0, 1, e);
+  // step s of (fa, fb): its operands are all read by now, so its stage takes the loads of
+  // step s + 3 while those of step s + 1 come from nxt: (fc, fa)
+  auto step = [&](Frag& fa, Frag& fb, Frag& fc, unsigned char* cur, unsigned char* nxt, int s) {
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0 & vm_wait(NL));   // step s + 1 landed; reads of step s arrived
+    bar();
+    begin_loads(s + 3);
+    phase(fa, fc, nxt, 0, true, cur);
+    phase(fb, fa, nxt, 1, false, nullptr);
+  };
+  int s = 0;
+  for (; s + 3 <= n; s += 3) {
+    step(f0, f1, f2, s0, s1, s);
+    step(f2, f0, f1, s1, s2, s + 1);
+    step(f1, f2, f0, s2, s0, s + 2);
+  }
+  if (s < n) step(f0, f1, f2, s0, s1, s);
+  if (s + 1 < n) step(f2, f0, f1, s1, s2, s + 1);
+  __builtin_amdgcn_s_waitcnt(0);   // loads and reads past the last step
+  bar();
+  mma_done(acc);
+  const int ow = GLU ? wmi * 64 : wmi * 128;
+  i8_finish_big<GLU>(acc, epi, T, O, o0 + ow, t0 + wni * 128, lane, s0 + wave * 8192, sw, ow);
 }
 
 template <int BM, int BN, int WM, int WN, bool SP, bool GLU, int NST>
@@ -410,8 +819,20 @@ hipError_t launch_cfg(const I8Args& a, int64_t splits, int32_t* part, hipStream_
 template <bool SP, bool GLU>
 hipError_t launch_kind(const I8Args& a, bool large, int64_t splits, int32_t* part, hipStream_t s) {
   if (large) {
-    if constexpr (GLU || SP) return launch_cfg<256, 256, 2, 4, SP, GLU, 2>(a, splits, part, s);
-    else return launch_cfg<256, 256, 4, 2, SP, GLU, 2>(a, splits, part, s);
+    if constexpr (SP) {
+      constexpr int BO = GLU ? 128 : 256;
+      const int64_t tm = (a.o + BO - 1) / BO, tn = (a.t + 255) / 256;
+      if (tm > 0x7FFFFFFF || tn > 0x7FFFFFFF || tm * tn > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+      k_i8_big<GLU><<<dim3((unsigned)(tm * tn)), dim3(256), 0, s>>>(
+          a.x, a.ldx, a.w, a.w_up, a.ldw, a.meta, a.up_meta, a.t, a.o, (int)a.k, a.epi, (int)tm, (int)tn,
+          (int)(tm < 8 ? tm : 8));
+      a.route.note(NM_TAKEN_TILE_LDS | NM_TAKEN_SPARSE_MMA);
+      return hipGetLastError();
+    } else if constexpr (GLU) {
+      return launch_cfg<256, 256, 2, 4, false, true, 2>(a, 1, nullptr, s);
+    } else {
+      return launch_cfg<256, 256, 4, 2, false, false, 2>(a, 1, nullptr, s);
+    }
   }
   if (a.t <= 64) return launch_cfg<128, 64, 4, 2, SP, GLU, 3>(a, splits, part, s);
   return launch_cfg<128, 128, 4, 2, SP, GLU, 3>(a, splits, part, s);
