@@ -188,26 +188,59 @@ __global__ __launch_bounds__(TB >= 4 ? 512 : 1024) void k_few_i8(
   }
 }
 
-// y from the splits' sums, part[split][matrix][t][o4]: one thread per 4 outputs.
+// y from the splits' sums, part[split][matrix][t][o4]: one thread per 4 outputs, every load of
+// up to 8 splits in flight together.  whole: O and ldy are multiples of 4.
 template <bool GLU>
-__global__ __launch_bounds__(256) void k_i8_reduce(const int32_t* __restrict__ part, int splits, int64_t T, int64_t O,
-                                                   I8Epi epi) {
-  const int64_t q = (O + 3) / 4, o4 = 4 * q;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void k_i8_reduce(const int32_t* __restrict__ part, int splits, uint32_t T, uint32_t O,
+                                                   I8Epi epi, int whole) {
+  const uint32_t q = (O + 3) / 4;
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
   if (i >= T * q) return;
-  const int64_t t = i / q, o = (i - t * q) * 4;
+  const uint32_t t = i / q, o = (i - t * q) * 4;
+  const int64_t mat = (int64_t)T * (4 * q), stride = (GLU ? 2 : 1) * mat;
+  const int32_t* p = part + 4 * (int64_t)i;
   i32x4 s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
-  const int32_t* p = part + t * o4 + o;
-  const int64_t mat = T * o4;
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    s0 += *reinterpret_cast<const i32x4*>(p);
-    if constexpr (GLU) s1 += *reinterpret_cast<const i32x4*>(p + mat);
-    p += (GLU ? 2 : 1) * mat;
-  }
+  for (int s = 0; s < splits; s += 8) {
+    i32x4 v0[8], v1[8];
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (o + r < O) i8_store<GLU>(epi, s0[r], s1[r], t, o + r);
+    for (int e = 0; e < 8; ++e) {
+      const bool in = s + e < splits;   // past the last split: the first again, not added
+      v0[e] = *reinterpret_cast<const i32x4*>(p + (in ? s + e : 0) * stride);
+      if constexpr (GLU) v1[e] = *reinterpret_cast<const i32x4*>(p + mat + (in ? s + e : 0) * stride);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (s + e >= splits) break;
+      s0 += v0[e];
+      if constexpr (GLU) s1 += v1[e];
+    }
+  }
+  if (!whole) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (o + r < O) i8_store<GLU>(epi, s0[r], s1[r], t, o + r);
+    return;
+  }
+  const float xs = epi.x_scale[t];
+  const f32x4 ws = *reinterpret_cast<const f32x4*>(epi.w_scale + o);
+  const bool shifted = !GLU && epi.col_shift != nullptr;
+  const float* ep = GLU ? epi.up_scale : epi.col_shift;
+  const f32x4 es = GLU || shifted ? *reinterpret_cast<const f32x4*>(ep + o) : f32x4{0.f, 0.f, 0.f, 0.f};
+  const float rb = shifted && epi.row_shift != nullptr ? epi.row_shift[t] : 1.f;
+  f32x4 v;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (!GLU && !shifted) v[r] = ((float)s0[r] * xs) * ws[r];
+    else v[r] = i8_value<GLU>(epi, s0[r], s1[r], xs, ws[r], es[r], rb, es[r]);
+  }
+  if (epi.bf16_out) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(epi.y) + t * epi.ldy + o) =
+        make_uint2(bf16_rne(v[0]) | (uint32_t)bf16_rne(v[1]) << 16, bf16_rne(v[2]) | (uint32_t)bf16_rne(v[3]) << 16);
+  } else {
+    f32x4* yp = reinterpret_cast<f32x4*>(static_cast<float*>(epi.y) + t * epi.ldy + o);
+    if (epi.accumulate) v += *yp;
+    *yp = v;
+  }
 }
 
 struct FewPlan {
@@ -269,10 +302,11 @@ hipError_t launch_i8_reduce(const int32_t* part, int64_t splits, bool glu, int64
                             const Route& r, hipStream_t s) {
   const int64_t n = t * ((o + 3) / 4);
   if (n <= 0) return hipSuccess;
-  if ((n + 255) / 256 > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (n > 0x3FFFFFFF) return hipErrorInvalidConfiguration;   // plans split far smaller outputs only
+  const int whole = o % 4 == 0 && e.ldy % 4 == 0;
   const dim3 grid((unsigned)((n + 255) / 256)), block(256);
-  if (glu) k_i8_reduce<true><<<grid, block, 0, s>>>(part, (int)splits, t, o, e);
-  else k_i8_reduce<false><<<grid, block, 0, s>>>(part, (int)splits, t, o, e);
+  if (glu) k_i8_reduce<true><<<grid, block, 0, s>>>(part, (int)splits, (uint32_t)t, (uint32_t)o, e, whole);
+  else k_i8_reduce<false><<<grid, block, 0, s>>>(part, (int)splits, (uint32_t)t, (uint32_t)o, e, whole);
   r.note(NM_TAKEN_REDUCE);
   return hipGetLastError();
 }

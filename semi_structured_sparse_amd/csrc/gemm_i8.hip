@@ -34,26 +34,70 @@ __device__ __forceinline__ void b2lds16(__amdgpu_buffer_rsrc_t r, void* lds, uin
 }
 constexpr uint32_t kPast = 0x80000000u;   // past every descriptor's range (< 2^31 bytes)
 
-// The two-stage K-loop: each step issues the next step's loads, multiplies, then waits for all
-// loads and synchronises.
+// K-loops over n >= 1 steps through NST stages (distinct static arrays, named by constant indices,
+// so that the compiler tracks the requests into each one).  issue(st, s) requests step s into
+// st, exactly L requests a wave.  Both end with every request landed and every stage free.
+
+// Two stages of large steps: a step's requests go out before the step ahead of it is multiplied
+// and are waited for after it.
 template <typename Issue, typename Compute>
-__device__ __forceinline__ void k_loop2(int n, unsigned char* a0, unsigned char* b0, unsigned char* a1, unsigned char* b1,
-                                        Issue&& issue, Compute&& compute) {
-  issue(a0, b0, 0);
+__device__ __forceinline__ void k_loop2(int n, unsigned char* a, unsigned char* b, Issue&& issue, Compute&& compute) {
+  issue(a, 0);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
   for (int s = 0; s < n; s += 2) {
-    if (s + 1 < n) issue(a1, b1, s + 1);
-    compute(a0, b0);
+    if (s + 1 < n) issue(b, s + 1);
+    compute(a);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     if (s + 1 < n) {
-      if (s + 2 < n) issue(a0, b0, s + 2);
-      compute(a1, b1);
+      if (s + 2 < n) issue(a, s + 2);
+      compute(b);
       __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
     }
   }
+}
+
+// Small steps: step q requests step q + NST - 1 into the stage that step q - 1 used, reads its
+// operands, all at once, and multiplies; then one wait (step q + 1 has landed) and one barrier.
+// Past the last step the last one is requested again; no one reads it.  (Reading operands a
+// step ahead, during the products, measured 2-6% slower; six stages, which leave a CU one
+// workgroup instead of two, 1-20% slower than four.)
+template <int NST, int L, typename Frag, typename Issue, typename Read, typename Mma>
+__device__ __forceinline__ void k_ring(int n, unsigned char* const (&S)[4], Issue&& issue, Read&& read, Mma&& mma) {
+  static_assert(NST >= 3 && NST <= 4 && L * (NST - 2) <= 63, "stages and requests per step");
+  auto bar = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+#pragma unroll
+    for (int j = 0; j + 1 < NST; ++j) issue(S[j], j < n ? j : n - 1);
+    __builtin_amdgcn_s_waitcnt(vm_wait(L * (NST - 2)));
+    bar();
+    auto step = [&](int j, int q) {   // j = q % NST, a constant after unrolling
+      const int ahead = q + NST - 1;
+      issue(S[(j + NST - 1) % NST], ahead < n ? ahead : n - 1);
+      Frag f;
+      read(f, S[j]);
+      __builtin_amdgcn_sched_barrier(0);
+      mma(f);
+      __builtin_amdgcn_s_waitcnt(vm_wait(L * (NST - 2)));
+      bar();
+    };
+    int s = 0;
+    for (; s + NST <= n; s += NST) {
+#pragma unroll
+      for (int j = 0; j < NST; ++j) step(j, s + j);
+    }
+#pragma unroll
+    for (int j = 0; j + 1 < NST; ++j) {
+      if (s + j >= n) break;
+      step(j, s + j);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    bar();
 }
 
 // Two fp32 values as packed bf16, to nearest even.
@@ -66,19 +110,18 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 
 // The output factors of a tile in LDS (requested before the K-loop: loaded after it they cost
 // 4 us a tile): w_scale, then up_scale (GLU) or col_shift of BO outputs, past O the last one.
-// Waves 0 .. 2 BO / 64 - 1 load 64 each.
+// Waves 0 .. 2 BO / 64 - 1 load 64 each (GLU tiles of 32 outputs: both halves of one load).
 template <int BO, bool GLU, int NW>
 __device__ __forceinline__ void load_factors(const I8Epi& epi, int64_t o0, int64_t O, int wave, int lane, float* sw) {
-  constexpr int PER = BO / 64;
+  static_assert(BO % 64 == 0 || (GLU && BO == 32), "a load of 64 factors is of one kind, or of two whole ones");
+  const float* const second = GLU ? epi.up_scale : epi.col_shift;
 #pragma unroll
-  for (int q = 0; q < (2 * PER + NW - 1) / NW; ++q) {
-    const int g = wave + q * NW;
-    if (g >= 2 * PER) break;
-    const float* src = g < PER ? epi.w_scale : GLU ? epi.up_scale : epi.col_shift;
-    if (src == nullptr) break;
-    int64_t o = o0 + (g % PER) * 64 + lane;
+  for (int q = 0; q < (2 * BO / 64 + NW - 1) / NW; ++q) {
+    const int g = wave + q * NW, e = g * 64 + lane;   // factor e: kind e / BO of output e % BO
+    if (g >= 2 * BO / 64 || (g * 64 >= BO && second == nullptr)) break;
+    int64_t o = o0 + e % BO;
     o = o < O ? o : O - 1;
-    __builtin_amdgcn_global_load_lds(src + o, (lds_void*)(sw + g * 64), 4, 0, 0);
+    __builtin_amdgcn_global_load_lds((e < BO ? epi.w_scale : second) + o, (lds_void*)(sw + g * 64), 4, 0, 0);
   }
 }
 
@@ -273,14 +316,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
   constexpr int V_BYTES = BM * AROW;
   constexpr int A_BYTES = V_BYTES + (SP ? BM * 16 : 0), B_BYTES = BN * 128;
   constexpr int NA = BM / RPG / NW, NB = BN / 8 / NW;
-  constexpr int NMW = SP ? BM / 64 : 0;        // waves that load positions (64 rows each)
-  static_assert(NA >= 1 && NB >= 1 && BM % (RPG * NW) == 0 && BN % (8 * NW) == 0 && NMW <= NW, "load groups per wave");
+  static_assert(NA >= 1 && NB >= 1 && BM % (RPG * NW) == 0 && BN % (8 * NW) == 0, "load groups per wave");
+  static_assert(!SP || BM == 16 * NW, "positions: 16 rows a wave, 4 bytes a lane");
   static_assert(!GLU || FI % 2 == 0, "GLU: gate and up blocks in one wave");
-  constexpr int A2 = NST >= 3 ? A_BYTES : 16, B2 = NST >= 3 ? B_BYTES : 16;
-  __shared__ __align__(16) unsigned char sA0[A_BYTES], sB0[B_BYTES];
-  __shared__ __align__(16) unsigned char sA1[A_BYTES], sB1[B_BYTES];
-  __shared__ __align__(16) unsigned char sA2[A2], sB2[B2];
-  __shared__ __align__(16) float sw[2 * (BO < 64 ? 64 : BO)];
+  constexpr int ST_BYTES = A_BYTES + B_BYTES;   // a stage: weight rows, positions, X rows
+  __shared__ __align__(16) unsigned char s0[ST_BYTES], s1[ST_BYTES], s2[NST > 2 ? ST_BYTES : 16], s3[NST > 3 ? ST_BYTES : 16];
+  unsigned char* const S[4] = {s0, s1, s2, s3};
+  __shared__ __align__(16) float sw[2 * BO];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wmi = wave % WM, wni = wave / WM;
@@ -331,14 +373,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
       if (q == 0) btail = last + 16 * c >= k ? kPast : 0u;
     }
   }
-  uint32_t moff = 0;
-  const uint8_t* mbase = nullptr;   // positions of the tile's rows in step block 0
+  const uint8_t* mlane = nullptr;   // the lane's four bytes of positions in step block 0
   if constexpr (SP) {
-    const int r = (wave < NMW ? wave : 0) * 64 + lane;
+    const int r = wave * 16 + (lane >> 2);
     int o = GLU ? (r >> 5) * 16 + (r & 15) : r;
     o = o < orows ? o : orows - 1;
-    moff = (uint32_t)(o * 16);
-    mbase = m0 + o0 * 16;
+    mlane = (GLU && (wave & 1) ? m1 : m0) + (o0 + o) * 16 + 4 * (lane & 3);
   }
 
   if (part == nullptr) load_factors<BO, GLU, NW>(epi, o0, O, wave, lane, sw);
@@ -349,7 +389,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
 #pragma unroll
     for (int j = 0; j < FJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
-  auto issue = [&](unsigned char* a, unsigned char* b, int si) {
+  auto issue = [&](unsigned char* a, int si) {
+    unsigned char* const b = a + A_BYTES;
     const int s = sb + si;
     const uint32_t at = s == steps_all - 1 ? atail : 0u, bt = s == steps_all - 1 ? btail : 0u;
 #pragma unroll
@@ -358,19 +399,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
       const bool second = GLU && ((SP ? grp : grp >> 1) & 1);
       b2lds16(second ? rw1 : rw0, a + grp * 1024, aoff[q] + at, (uint32_t)(s * AROW));
     }
-    if constexpr (SP) {
-      if (wave < NMW) {
-        const uint8_t* mp = mbase + (int64_t)s * O * 16;
-        if constexpr (GLU) {
-          // rows alternate between the two weights in blocks of 16: a pointer per lane
-          const uint8_t* up = m1 + o0 * 16 + (int64_t)s * O * 16;
-          const uint8_t* src = ((lane >> 4) & 1 ? up : mp) + moff;
-          __builtin_amdgcn_global_load_lds(src, (lds_void*)(a + V_BYTES + wave * 1024), 16, 0, 0);
-        } else {
-          __builtin_amdgcn_global_load_lds(mp + moff, (lds_void*)(a + V_BYTES + wave * 1024), 16, 0, 0);
-        }
-      }
-    }
+    if constexpr (SP)
+      __builtin_amdgcn_global_load_lds(mlane + (int64_t)s * O * 16, (lds_void*)(a + V_BYTES + wave * 256), 4, 0, 0);
 #pragma unroll
     for (int q = 0; q < NB; ++q) b2lds16(rx, b + (wave + q * NW) * 1024, boff[q] + bt, (uint32_t)(s * 128));
   };
@@ -379,84 +409,96 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
     const int r = wni * SN + j * 16 + fr;
     return *reinterpret_cast<const i32x4*>(b + r * 128 + 16 * swz8(r, 4 * ks + fq));
   };
-  auto compute = [&](const unsigned char* a, const unsigned char* b) {
-    if constexpr (SP) {
-      i32x4 af[FI];
-      int idx[FI];
+  // 256-row tiles (dense): an A fragment a row block ahead, the second half's B fragments during
+  // the first
+  auto compute = [&](const unsigned char* a) {
+    const unsigned char* const b = a + A_BYTES;
+    auto read_a = [&](int ks, int i) {
+      const int r = wmi * SM + i * 16 + fr;
+      return *reinterpret_cast<const i32x4*>(a + r * 128 + 16 * swz8(r, 4 * ks + fq));
+    };
+    i32x4 b0[FJ], b1[FJ];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) b0[j] = read_b(b, 0, j);
+    i32x4 acur = read_a(0, 0), anxt;
+    constexpr int BPS = (FJ + FI - 1) / FI;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
       for (int i = 0; i < FI; ++i) {
-        const int r = wmi * SM + i * 16 + fr;
-        af[i] = *reinterpret_cast<const i32x4*>(a + r * 64 + 16 * swz4(r, fq));
-        idx[i] = *reinterpret_cast<const int*>(a + V_BYTES + r * 16 + 4 * fq);
-      }
-      i32x4 lo = read_b(b, 0, 0), hi = read_b(b, 1, 0), nlo, nhi;
-#pragma unroll
-      for (int j = 0; j < FJ; ++j) {
         __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
         __builtin_amdgcn_sched_barrier(0);
-        if (j + 1 < FJ) {
-          nlo = read_b(b, 0, j + 1);
-          nhi = read_b(b, 1, j + 1);
+        if (i + 1 < FI) anxt = read_a(ks, i + 1);
+        else if (ks == 0) anxt = read_a(1, 0);
+        if (ks == 0) {
+#pragma unroll
+          for (int q = 0; q < BPS; ++q)
+            if (i * BPS + q < FJ) b1[i * BPS + q] = read_b(b, 1, i * BPS + q);
         }
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
-        const i32x8 bv = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-        for (int i = 0; i < FI; ++i)
-          acc[i][j] = __builtin_amdgcn_smfmac_i32_16x16x128_i8(af[i], bv, acc[i][j], idx[i], 0, 0);
+        for (int j = 0; j < FJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(acur, ks ? b1[j] : b0[j], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
-        lo = nlo;
-        hi = nhi;
+        acur = anxt;
       }
-    } else {
-      auto read_a = [&](int ks, int i) {
-        const int r = wmi * SM + i * 16 + fr;
-        return *reinterpret_cast<const i32x4*>(a + r * 128 + 16 * swz8(r, 4 * ks + fq));
-      };
-      i32x4 b0[FJ], b1[FJ];
+    }
+  };
+  // smaller tiles: the operands of a whole step at once, a step ahead (k_ring)
+  constexpr int KS = SP ? 1 : 2;
+  struct Frag {
+    i32x4 a[KS][FI], b0[FJ], b1[FJ];
+    int idx[SP ? FI : 1];
+  };
+  auto read = [&](Frag& f, const unsigned char* a) {
 #pragma unroll
-      for (int j = 0; j < FJ; ++j) b0[j] = read_b(b, 0, j);
-      i32x4 acur = read_a(0, 0), anxt;
-      constexpr int BPS = (FJ + FI - 1) / FI;
+    for (int i = 0; i < FI; ++i) {
+      const int r = wmi * SM + i * 16 + fr;
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
+      for (int ks = 0; ks < KS; ++ks)
+        f.a[ks][i] = *reinterpret_cast<const i32x4*>(a + r * AROW + 16 * (SP ? swz4(r, fq) : swz8(r, 4 * ks + fq)));
+      if constexpr (SP) f.idx[i] = *reinterpret_cast<const int*>(a + V_BYTES + r * 16 + 4 * fq);
+    }
 #pragma unroll
-        for (int i = 0; i < FI; ++i) {
-          __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-          __builtin_amdgcn_sched_barrier(0);
-          if (i + 1 < FI) anxt = read_a(ks, i + 1);
-          else if (ks == 0) anxt = read_a(1, 0);
-          if (ks == 0) {
+    for (int j = 0; j < FJ; ++j) {
+      f.b0[j] = read_b(a + A_BYTES, 0, j);
+      f.b1[j] = read_b(a + A_BYTES, 1, j);
+    }
+  };
+  auto mma = [&](const Frag& f) {
 #pragma unroll
-            for (int q = 0; q < BPS; ++q)
-              if (i * BPS + q < FJ) b1[i * BPS + q] = read_b(b, 1, i * BPS + q);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-          __builtin_amdgcn_s_setprio(1);
+    for (int j = 0; j < FJ; ++j)
 #pragma unroll
-          for (int j = 0; j < FJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(acur, ks ? b1[j] : b0[j], acc[i][j], 0, 0, 0);
-          __builtin_amdgcn_s_setprio(0);
-          __builtin_amdgcn_sched_barrier(0);
-          acur = anxt;
+      for (int i = 0; i < FI; ++i) {
+        if constexpr (SP) {
+          const i32x8 bv = __builtin_shufflevector(f.b0[j], f.b1[j], 0, 1, 2, 3, 4, 5, 6, 7);
+          acc[i][j] = __builtin_amdgcn_smfmac_i32_16x16x128_i8(f.a[0][i], bv, acc[i][j], f.idx[i], 0, 0);
+        } else {
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[0][i], f.b0[j], acc[i][j], 0, 0, 0);
         }
       }
+    if constexpr (!SP) {
+#pragma unroll
+      for (int j = 0; j < FJ; ++j)
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[KS - 1][i], f.b1[j], acc[i][j], 0, 0, 0);
     }
   };
   if (n > 0) {
     if constexpr (NST == 2) {
-      k_loop2(n, sA0, sB0, sA1, sB1, issue, compute);
+      static_assert(!SP, "2:4 products of this size: k_i8_big");
+      k_loop2(n, s0, s1, issue, compute);
     } else {
-      unsigned char* const SA[3] = {sA0, sA1, sA2};
-      unsigned char* const SB[3] = {sB0, sB1, sB2};
-      lds_ring<NST, NA + NB>(n, SA, SB, issue, compute);
+      k_ring<NST, NA + NB + (SP ? 1 : 0), Frag>(n, S, issue, read, mma);
     }
   }
 
-  constexpr int TURN = (GLU ? FI / 2 : FI) % 4 != 0 ? 0 : B_BYTES >= NW * 4096 ? 4096 : 0;
+  constexpr int TURN = (GLU ? FI / 2 : FI) % 4 != 0 ? 0 : ST_BYTES >= NW * 8192 ? 8192 : ST_BYTES >= NW * 4096 ? 4096 : 0;
   const int ow = GLU ? wmi * SM / 2 : wmi * SM;
-  i8_finish<FI, FJ, GLU, TURN>(acc, epi, part, kpart, T, O, o0 + ow, t0 + wni * SN, lane, sB0 + wave * TURN, sw, BO, ow);
+  i8_finish<FI, FJ, GLU, TURN>(acc, epi, part, kpart, T, O, o0 + ow, t0 + wni * SN, lane, s0 + wave * TURN, sw, BO, ow);
 }
 
 // ----------------------------------------------------------- the large 2:4 products ---
@@ -817,8 +859,8 @@ hipError_t launch_cfg(const I8Args& a, int64_t splits, int32_t* part, hipStream_
 }
 
 template <bool SP, bool GLU>
-hipError_t launch_kind(const I8Args& a, bool large, int64_t splits, int32_t* part, hipStream_t s) {
-  if (large) {
+hipError_t launch_kind(const I8Args& a, int shape, int64_t splits, int32_t* part, hipStream_t s) {
+  if (shape < 0) {
     if constexpr (SP) {
       constexpr int BO = GLU ? 128 : 256;
       const int64_t tm = (a.o + BO - 1) / BO, tn = (a.t + 255) / 256;
@@ -834,17 +876,47 @@ hipError_t launch_kind(const I8Args& a, bool large, int64_t splits, int32_t* par
       return launch_cfg<256, 256, 4, 2, false, false, 2>(a, 1, nullptr, s);
     }
   }
-  if (a.t <= 64) return launch_cfg<128, 64, 4, 2, SP, GLU, 3>(a, splits, part, s);
-  return launch_cfg<128, 128, 4, 2, SP, GLU, 3>(a, splits, part, s);
+  switch (shape) {
+    case 0: return launch_cfg<128, 128, 4, 2, SP, GLU, 3>(a, splits, part, s);
+    case 1: return launch_cfg<128, 64, 4, 2, SP, GLU, 4>(a, splits, part, s);
+    case 2: return launch_cfg<64, 64, 2, 2, SP, GLU, 4>(a, splits, part, s);
+  }
+  return launch_cfg<64, 32, 2, 2, SP, GLU, 4>(a, splits, part, s);
 }
 
-// splits of the 128-row tiles: one workgroup per CU, at least two steps each
-int64_t mid_splits(int64_t t, int64_t o, int64_t k, bool glu) {
-  const int64_t bn = t <= 64 ? 64 : 128, bo = glu ? 64 : 128;
-  const int64_t tiles = ((o + bo - 1) / bo) * ((t + bn - 1) / bn), steps = (k + 127) / 128;
-  int64_t s = tiles > 0 ? 256 / tiles : 1;
-  if (s > steps / 2) s = steps / 2;
-  return s < 1 ? 1 : s;
+struct MidPlan {
+  int shape;        // 128 x 128, 128 x 64, 64 x 64, 64 x 32 (weight rows x tokens)
+  int64_t splits;
+};
+
+// The largest tile that gives 192 workgroups; with none, the smallest, the reduction cut in
+// ranges of at least two steps up to one workgroup per CU.  A split costs the partial sums and
+// a second kernel (4-5 us at 61 x 4096 x 14336), so it is the last choice, except that 64 x 32
+// tiles pay 0.15 us for each step however little it holds: over 64 steps, 64 x 64 tiles in two
+// ranges.  Measured (us; 128 x 128 / 128 x 64 / 64 x 64 / 64 x 32, split to fill the chip):
+// dense 61 x 4096 x 14336 18.9 / 18.0 / 16.2 / 15.5, 777 x 1025 x 1999 17.0 / 14.0 / 10.7 /
+// 10.6, 128 x 4096 x 4096 17.8 / 13.8 / 11.1 / 9.6, 512 x 4096 x 4096 20.0 / 17.3 / 19.1 / 23.1,
+// 2048^3 19.0 / 22.4 / 23.4 / 27.2; 2:4 333 x 4096 x 6144 19.6 / 19.4 / 22.2 / 22.2,
+// 128 x 4096 x 14336 20.3 / 17.0 / 17.0 / 20.5, 1024 x 4096 x 4096 24.3 / 27.1 / 31.8 / 39.1.
+MidPlan mid_plan(int64_t t, int64_t o, int64_t k, bool glu) {
+  const int64_t steps = (k + 127) / 128;
+  const int bm[4] = {128, 128, 64, 64}, bn[4] = {128, 64, 64, 32};
+  auto tiles = [&](int sh) {
+    const int64_t bo = glu ? bm[sh] / 2 : bm[sh];
+    return ((o + bo - 1) / bo) * ((t + bn[sh] - 1) / bn[sh]);
+  };
+  MidPlan p{3, 1};
+  if (t > 32) {
+    for (int sh = 0; sh < 4; ++sh) {
+      if (tiles(sh) < 192) continue;
+      if (sh == 3 && steps > 64) return {2, 2};
+      return {sh, 1};
+    }
+  }
+  p.splits = tiles(3) > 0 ? 256 / tiles(3) : 1;
+  if (p.splits > steps / 2) p.splits = steps / 2;
+  if (p.splits < 1) p.splits = 1;
+  return p;
 }
 
 }  // namespace
@@ -857,18 +929,21 @@ bool i8_tile_eligible(const I8Args& a) {
 }
 
 int64_t i8_mid_part_bytes(int64_t t, int64_t o, int64_t k, bool glu) {
-  const int64_t s = mid_splits(t, o, k, glu);
+  const int64_t s = mid_plan(t, o, k, glu).splits;
   return s > 1 ? s * (glu ? 2 : 1) * t * ((o + 3) / 4 * 4) * 4 : 0;
 }
 
 hipError_t launch_i8_tile(const I8Args& a, bool large, int32_t* part, int64_t part_bytes, hipStream_t s) {
   const bool sp = a.meta != nullptr, glu = a.glu != 0;
-  int64_t splits = 1;
-  if (!large && part != nullptr && part_bytes >= i8_mid_part_bytes(a.t, a.o, a.k, glu)) splits = mid_splits(a.t, a.o, a.k, glu);
-  if (sp && glu) return launch_kind<true, true>(a, large, splits, part, s);
-  if (sp) return launch_kind<true, false>(a, large, splits, part, s);
-  if (glu) return launch_kind<false, true>(a, large, splits, part, s);
-  return launch_kind<false, false>(a, large, splits, part, s);
+  MidPlan p{-1, 1};   // 256 x 256 tiles
+  if (!large) {
+    p = mid_plan(a.t, a.o, a.k, glu);
+    if (part == nullptr || part_bytes < i8_mid_part_bytes(a.t, a.o, a.k, glu)) p.splits = 1;
+  }
+  if (sp && glu) return launch_kind<true, true>(a, p.shape, p.splits, part, s);
+  if (sp) return launch_kind<true, false>(a, p.shape, p.splits, part, s);
+  if (glu) return launch_kind<false, true>(a, p.shape, p.splits, part, s);
+  return launch_kind<false, false>(a, p.shape, p.splits, part, s);
 }
 
 }  // namespace nml
