@@ -68,21 +68,23 @@ __device__ __forceinline__ uint32_t max2(uint32_t mk, uint32_t d) {
 }
 
 // A thread's unit: PU pieces of 8 values (16 bytes of input, 8 bytes of codes), the least that
-// holds whole groups.  NT threads per row (64: a row per wave, 256 / 64 rows a workgroup), UN
-// units per thread.  SEL: 0 none, M the group width (NK > 0: n known at compile time).
-// LIFT: 0 none, 4 the N = 4 lift from registers, 1 any N through LDS (NT >= 256).
-template <int NT, int UN, int SEL, int NK, int LIFT>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_quant_i8(
+// holds whole groups; UN units per thread, the workgroup as many waves as the row needs (an
+// idle unit costs its loads' and its network's instructions: 8192 x 4096 at 5:16 took 41 us with
+// half of them idle, 25 with none).  WAVE: a row per wave, four rows a workgroup.
+// SEL: 0 none, M the group width (NK > 0: n known at compile time).  LIFT: 0 none, 4 the N = 4
+// lift from registers, 1 any N through LDS.
+template <bool WAVE, int UN, int SEL, int NK, int LIFT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_quant_i8(
     const uint16_t* __restrict__ x, int64_t rows, int k, int64_t ldx, int n, int ns, int8_t* __restrict__ q, int64_t ldq,
     float* __restrict__ scale) {
   constexpr int PU = SEL > 8 ? SEL / 8 : 1;
-  constexpr int RPB = NT < 256 ? 256 / NT : 1;   // rows per workgroup
-  constexpr int NW = NT / 64;                    // waves per row
-  __shared__ uint32_t red[NW > 1 ? NW : 1];
-  extern __shared__ __align__(16) unsigned char row_codes[];   // LIFT == 1: the row's codes
-  const int tid = RPB > 1 ? (int)(threadIdx.x % NT) : (int)threadIdx.x;
-  const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / NT : 0);
-  if (RPB > 1 && row >= rows) return;   // whole waves; no barrier below for these
+  __shared__ uint32_t red[WAVE ? 1 : 16];
+  extern __shared__ __align__(16) unsigned char codes[];   // LIFT == 1: the rows' codes
+  const int NT = WAVE ? 64 : (int)blockDim.x;              // threads of a row
+  const int tid = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (WAVE && row >= rows) return;   // whole waves; no barrier below for these
+  unsigned char* const row_codes = codes + (WAVE ? (threadIdx.x >> 6) * ((k + 15) / 16 * 16) : 0);
   const uint16_t* xr = x + row * ldx;
   int8_t* qr = q + row * ldq;
   const int units = (k + 8 * PU - 1) / (8 * PU);
@@ -148,12 +150,11 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_quant_i8(
     const uint32_t o = (uint32_t)__shfl_xor((int)mk, off, 64);
     mk = o > mk ? o : mk;
   }
-  if constexpr (NW > 1) {
+  if constexpr (!WAVE) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mk;
     __syncthreads();
     mk = red[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) mk = red[w] > mk ? red[w] : mk;
+    for (int w = 1; w < (int)(blockDim.x >> 6); ++w) mk = red[w] > mk ? red[w] : mk;
   }
   const RowScale rs = row_scale(mk);
   if (tid == 0) scale[row] = rs.scale;
@@ -189,7 +190,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_quant_i8(
     if (tid < (kl16 - kl) / 4) reinterpret_cast<uint32_t*>(qr + kl)[tid] = 0u;
   }
   if constexpr (LIFT == 1) {
-    __syncthreads();
+    if constexpr (WAVE) __builtin_amdgcn_wave_barrier();
+    else __syncthreads();
     const uint32_t wpg = (uint32_t)(ns - 1);
     const int dwords = k / (2 * ns) * (ns - 1);
     const int quads = (dwords + 3) / 4;
@@ -209,31 +211,30 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_quant_i8(
   }
 }
 
-template <int NT, int UN, int SEL, int NK, int LIFT>
-hipError_t launch_q(const uint16_t* x, int64_t rows, int64_t k, int64_t ldx, int n, int ns, int8_t* q, int64_t ldq,
-                    float* scale, hipStream_t s) {
-  constexpr int RPB = NT < 256 ? 256 / NT : 1;
-  const int64_t blocks = (rows + RPB - 1) / RPB;
-  const size_t lds = LIFT == 1 ? (size_t)((k + 15) / 16 * 16) : 0;
-  k_quant_i8<NT, UN, SEL, NK, LIFT><<<dim3((unsigned)blocks), dim3(NT < 256 ? 256 : NT), lds, s>>>(
+template <bool WAVE, int UN, int SEL, int NK, int LIFT>
+hipError_t launch_q(int threads, const uint16_t* x, int64_t rows, int64_t k, int64_t ldx, int n, int ns, int8_t* q,
+                    int64_t ldq, float* scale, hipStream_t s) {
+  const int64_t blocks = WAVE ? (rows + 3) / 4 : rows;
+  const size_t lds = LIFT == 1 ? (size_t)((k + 15) / 16 * 16) * (WAVE ? 4 : 1) : 0;
+  k_quant_i8<WAVE, UN, SEL, NK, LIFT><<<dim3((unsigned)blocks), dim3(WAVE ? 256 : threads), lds, s>>>(
       x, rows, (int)k, ldx, n, ns, q, ldq, scale);
   return hipGetLastError();
 }
 
-// Threads per row and units per thread by the row length (values held per thread: 8 PU UN).
+// A row per wave up to 2048 values (4 pieces a lane); longer rows 2 pieces a thread up to 4096 values
+// (4 for groups of 32, whose unit is 4), 4 up to 32768, 8 beyond.
 template <int SEL, int NK, int LIFT>
 hipError_t by_length(const uint16_t* x, int64_t rows, int64_t k, int64_t ldx, int n, int ns, int8_t* q, int64_t ldq,
                      float* scale, hipStream_t s) {
   constexpr int PU = SEL > 8 ? SEL / 8 : 1;
-#define NM_Q(NT, PIECES) return launch_q<NT, PIECES / PU, SEL, NK, LIFT>(x, rows, k, ldx, n, ns, q, ldq, scale, s)
-  if constexpr (LIFT != 1) {
-    if (k <= 64 * 8 * 4) NM_Q(64, 4);
+  if (k <= 2048) return launch_q<true, 4 / PU, SEL, NK, LIFT>(256, x, rows, k, ldx, n, ns, q, ldq, scale, s);
+  const int pieces = PU <= 2 && k <= 4096 ? 2 : k <= 32768 ? 4 : 8;
+  const int threads = (int)(((k + 15) / 16 * 16 + 512 * pieces - 1) / (512 * pieces) * 64);
+  if constexpr (PU <= 2) {
+    if (pieces == 2) return launch_q<false, 2 / PU, SEL, NK, LIFT>(threads, x, rows, k, ldx, n, ns, q, ldq, scale, s);
   }
-  if (k <= 256 * 8 * 4) NM_Q(256, 4);
-  if (k <= 256 * 8 * 8) NM_Q(256, 8);
-  if (k <= 1024 * 8 * 4) NM_Q(1024, 4);
-  NM_Q(1024, 8);
-#undef NM_Q
+  if (pieces == 4) return launch_q<false, 4 / PU, SEL, NK, LIFT>(threads, x, rows, k, ldx, n, ns, q, ldq, scale, s);
+  return launch_q<false, 8 / PU, SEL, NK, LIFT>(threads, x, rows, k, ldx, n, ns, q, ldq, scale, s);
 }
 
 // One thread per 16 bytes of output: block s of row r holds the positions of slots
