@@ -194,22 +194,34 @@ def _ld(t, default=0):
 
 
 _current_raw_stream = None      # () -> raw current stream of the current device
+_current_device = None          # () -> the current device
+
+
+def _bind_torch():
+    global _current_raw_stream, _current_device
+    import torch
+    torch.cuda.current_stream()             # initialises the device
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    # building a Stream object costs 2.7 us a call, the raw handle 0.2 us (one-token calls take 6)
+    if raw is not None and device is not None:
+        _current_raw_stream, _current_device = (lambda: raw(device())), device
+    else:
+        _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        _current_device = torch.cuda.current_device
 
 
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    global _current_raw_stream
     if _current_raw_stream is None:
-        import torch
-        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
-        torch.cuda.current_stream()             # initialises the device
-        # building a Stream object costs 2.7 us a call, the raw handle 0.2 us (one-token calls take 6)
-        if raw is not None and device is not None:
-            _current_raw_stream = lambda: raw(device())  # noqa: E731
-        else:
-            _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        _bind_torch()
     return _current_raw_stream()
+
+
+def _device():
+    if _current_device is None:
+        _bind_torch()
+    return _current_device()
 
 
 def _check(status: int, where: str):
@@ -478,27 +490,79 @@ def nm_hybrid_gemm(x, sparse_cols, k_s, dense_cols, k_d, ws_values, ws_meta, fmt
 
 # ------------------------------------------------------------------------ int8 layers ---
 
+def _device_of(*ts):
+    """The device the tensors have to be on where the caller names a stream; -1 where all of them
+    are raw pointers."""
+    for t in ts:
+        if t is not None and type(t) is not int:
+            if t.get_device() < 0:
+                _refuse(t, 0, "")
+            return _device()
+    return -1
+
+
+def _refuse(t, dev, what):
+    if t.get_device() != dev:
+        raise ValueError("tensors must be on the current GPU")
+    raise ValueError(what)
+
+
+def _vec(t, dev):
+    """Pointer of a tensor on device dev (None -> NULL, integers are raw pointers)."""
+    if t is None or type(t) is int:
+        return t
+    if t.get_device() != dev:
+        _refuse(t, dev, "")
+    return t.data_ptr()
+
+
+def _mat(t, dev, size=0):
+    """(pointer, leading dimension) of a matrix with contiguous rows (of `size`-byte elements)."""
+    if t is None or type(t) is int:
+        return t, 0
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1 or t.get_device() != dev or (size and t.element_size() != size):
+        _refuse(t, dev, f"a matrix with contiguous rows{f' of {size}-byte elements' if size else ''} is needed")
+    return t.data_ptr(), st[0]
+
+
+def _factors(t, n, dev):
+    """_vec of at least n contiguous fp32 values."""
+    if t is None or type(t) is int:
+        return t
+    if t.get_device() != dev or t.numel() < n or t.element_size() != 4 or not t.is_contiguous():
+        _refuse(t, dev, f"{n} contiguous fp32 factors are needed")
+    return t.data_ptr()
+
+
 def _i8_out(y):
     """NM_Y_* of an output tensor (raw pointers: fp32)."""
-    return NM_Y_BF16 if not isinstance(y, int) and y is not None and y.element_size() == 2 else NM_Y_F32
+    return NM_Y_BF16 if y is not None and type(y) is not int and y.element_size() == 2 else NM_Y_F32
 
 
 def _bytes(t):
-    return 0 if t is None or isinstance(t, int) else t.numel() * t.element_size()
+    return 0 if t is None or type(t) is int else t.numel() * t.element_size()
 
 
 def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, ldx=None, ldq=None, check=True):
-    rows = x.shape[0] if rows is None else rows
-    k = x.shape[1] if k is None else k
-    st = lib().nm_quant_i8(_ptr(x), rows, k, _ld(x) if ldx is None else ldx, n, m, ns, _ptr(q),
-                           _ld(q) if ldq is None else ldq, _ptr(scale), _stream(stream))
-    if check:
+    """Rows of bf16 x -> int8 codes q and one fp32 scale per row (include/nm.h)."""
+    dev = _device() if stream is None else _device_of(x, q, scale)
+    xp, lx = _mat(x, dev, 2)
+    qp, lq = _mat(q, dev, 1)
+    if rows is None:
+        rows = x.shape[0]
+    if k is None:
+        k = x.shape[1]
+    st = lib().nm_quant_i8(xp, rows, k, lx if ldx is None else ldx, n, m, ns, qp, lq if ldq is None else ldq,
+                           _factors(scale, rows, dev), _stream(stream))
+    if check and st:
         _check(st, "nm_quant_i8")
     return st
 
 
 def nm_meta_block(meta, o, kc, out, stream=None, *, check=True):
-    st = lib().nm_meta_block(_ptr(meta), o, kc, _ptr(out), _stream(stream))
+    dev = _device() if stream is None else _device_of(meta, out)
+    st = lib().nm_meta_block(_vec(meta, dev), o, kc, _vec(out, dev), _stream(stream))
     if check:
         _check(st, "nm_meta_block")
     return st
@@ -515,15 +579,26 @@ def nm_i8_workspace_size(t: int, o: int, k: int, sparse: bool = False, glu: bool
 def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift=None, accumulate=0, workspace=None,
                stream=None, *, t=None, o=None, k=None, ldx=None, ldw=None, ldy=None, y_dtype=None,
                workspace_bytes=None, route=0, taken=None, check=True):
-    """taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
-    st = lib().nm_spmm_i8(_ptr(x), x.shape[0] if t is None else t, x.shape[1] if k is None else k,
-                          _ld(x) if ldx is None else ldx, _ptr(x_scale), _ptr(w), w.shape[0] if o is None else o,
-                          _ld(w) if ldw is None else ldw, _ptr(w_scale), _ptr(w_meta), _ptr(row_shift),
-                          _ptr(col_shift), _ptr(y), _ld(y) if ldy is None else ldy,
-                          _i8_out(y) if y_dtype is None else y_dtype, accumulate, _ptr(workspace),
-                          _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
+    """y = (x . w^T) * x_scale * w_scale (+ row_shift * col_shift) in 8-bit integers; w_meta (from
+    nm_meta_block): 2:4 weights.  k: the reduction length where it is not x's width.
+    taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
+    dev = _device() if stream is None else _device_of(x, w, y)
+    xp, lx = _mat(x, dev, 1)
+    wp, lw = _mat(w, dev, 1)
+    yp, ly = _mat(y, dev)
+    if t is None:
+        t = x.shape[0]
+    if o is None:
+        o = w.shape[0]
+    if k is None:
+        k = x.shape[1]
+    st = lib().nm_spmm_i8(xp, t, k, lx if ldx is None else ldx, _factors(x_scale, t, dev), wp, o,
+                          lw if ldw is None else ldw, _factors(w_scale, o, dev), _vec(w_meta, dev),
+                          _factors(row_shift, t, dev), _factors(col_shift, o, dev), yp,
+                          ly if ldy is None else ldy, _i8_out(y) if y_dtype is None else y_dtype, accumulate,
+                          _vec(workspace, dev), _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
                           ctypes.addressof(taken) if taken is not None else None, _stream(stream))
-    if check:
+    if check and st:
         _check(st, "nm_spmm_i8")
     return st
 
@@ -531,18 +606,29 @@ def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift
 def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU, gate_meta=None, up_meta=None,
               workspace=None, stream=None, *, t=None, inter=None, k=None, ldx=None, ldw=None, ldy=None, y_dtype=None,
               workspace_bytes=None, route=0, taken=None, check=True):
-    """taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
+    """y = act(x . w_gate^T) * (x . w_up^T), each with its scales, in 8-bit integers.
+    taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
+    dev = _device() if stream is None else _device_of(x, w_gate, y)
+    xp, lx = _mat(x, dev, 1)
+    gp, lg = _mat(w_gate, dev, 1)
+    up, lu = _mat(w_up, dev, 1)
+    yp, ly = _mat(y, dev)
     if ldw is None:
-        ldw = _ld(w_gate)
-        if _ld(w_up) != ldw:
+        if lg != lu:
             raise ValueError("w_gate and w_up need the same leading dimension")
-    st = lib().nm_glu_i8(_ptr(x), x.shape[0] if t is None else t, x.shape[1] if k is None else k,
-                         _ld(x) if ldx is None else ldx, _ptr(x_scale), _ptr(w_gate), _ptr(gate_scale),
-                         _ptr(gate_meta), _ptr(w_up), _ptr(up_scale), _ptr(up_meta),
-                         w_gate.shape[0] if inter is None else inter, ldw, act, _ptr(y),
-                         _ld(y) if ldy is None else ldy, _i8_out(y) if y_dtype is None else y_dtype, _ptr(workspace),
+        ldw = lg
+    if t is None:
+        t = x.shape[0]
+    if inter is None:
+        inter = w_gate.shape[0]
+    if k is None:
+        k = x.shape[1]
+    st = lib().nm_glu_i8(xp, t, k, lx if ldx is None else ldx, _factors(x_scale, t, dev), gp,
+                         _factors(gate_scale, inter, dev), _vec(gate_meta, dev), up,
+                         _factors(up_scale, inter, dev), _vec(up_meta, dev), inter, ldw, act, yp,
+                         ly if ldy is None else ldy, _i8_out(y) if y_dtype is None else y_dtype, _vec(workspace, dev),
                          _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
                          ctypes.addressof(taken) if taken is not None else None, _stream(stream))
-    if check:
+    if check and st:
         _check(st, "nm_glu_i8")
     return st

@@ -220,3 +220,24 @@ def test_sums_are_exact_integers():
     g = np.array([-3.0, 0.0, 2.0])
     for v, z in zip(g, O.glu_gate(g, "gelu")):
         assert abs(z - 0.5 * v * (1 + math.tanh(math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)))) < 1e-15
+
+
+def test_binding_refuses_tensors_that_are_not_on_the_gpu_or_do_not_fit():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    q, s = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4)
+    with pytest.raises(ValueError, match="current GPU"):
+        S.nm_quant_i8(x, q, s, stream=0)
+    with pytest.raises(ValueError, match="current GPU"):
+        S.nm_spmm_i8(q, s, q, s, torch.zeros(4, 4), stream=0)
+    with pytest.raises(ValueError, match="current GPU"):
+        S.nm_glu_i8(q, s, q, s, q, s, torch.zeros(4, 4), stream=0)
+    with pytest.raises(ValueError, match="current GPU"):
+        S.nm_meta_block(q, 4, 64, q, stream=0)
+
+
+def test_errors_raise_by_default():
+    with pytest.raises(S.NMError, match="NM_EINVAL"):
+        S.nm_spmm_i8(P, None, Q, P, R, t=1, o=1, k=16, ldx=16, ldw=16, ldy=1, stream=0)
+    with pytest.raises(S.NMError, match="NM_EALIGN"):
+        S.nm_quant_i8(MIS, Q, R, rows=1, k=16, ldx=16, ldq=16, stream=0)

@@ -544,3 +544,18 @@ def test_same_buffers_twice():
         S.nm_glu_i8(x, xs, wd, scd, wd, scd, g.y)
         ys.append(g.get())
     assert np.array_equal(ys[0], ys[1]) and np.array_equal(ys[0], ys[2])
+
+
+def test_binding_refuses_what_does_not_fit():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    q, s = torch.zeros(4, 64, dtype=torch.int8, device="cuda"), torch.zeros(4, device="cuda")
+    y = torch.zeros(4, 4, device="cuda")
+    for bad in (lambda: S.nm_quant_i8(x.float(), q, s), lambda: S.nm_quant_i8(x, x, s), lambda: S.nm_quant_i8(x.t(), q, s),
+                lambda: S.nm_quant_i8(x, q, s[:3]), lambda: S.nm_quant_i8(x, q, s.double()),
+                lambda: S.nm_quant_i8(x, q.cpu(), s), lambda: S.nm_spmm_i8(q, s[:3], q, s, y),
+                lambda: S.nm_spmm_i8(q, s, q, s[::2], y), lambda: S.nm_spmm_i8(x, s, q, s, y),
+                lambda: S.nm_spmm_i8(q, s, q, s, y.cpu()), lambda: S.nm_spmm_i8(q, s, q, s, y, col_shift=s[:2]),
+                lambda: S.nm_spmm_i8(q, s, q, s, y, workspace=q.cpu()), lambda: S.nm_glu_i8(q, s, q, s, q.t(), s, y),
+                lambda: S.nm_glu_i8(q, s, q, s, torch.zeros(4, 128, dtype=torch.int8, device="cuda"), s, y)):
+        with pytest.raises(ValueError):
+            bad()
