@@ -34,6 +34,12 @@ __device__ __forceinline__ void b2lds16(__amdgpu_buffer_rsrc_t r, void* lds, uin
 }
 constexpr uint32_t kPast = 0x80000000u;   // past every descriptor's range (< 2^31 bytes)
 
+// A stage: the weight rows (and positions) and the X rows of a step, arrays of their own (as one
+// array, 8192 x 14336 x 4096 took 433 us instead of 389).
+struct Stage {
+  unsigned char *a, *b;
+};
+
 // K-loops over n >= 1 steps through NST stages (distinct static arrays, named by constant indices,
 // so that the compiler tracks the requests into each one).  issue(st, s) requests step s into
 // st, exactly L requests a wave.  Both end with every request landed and every stage free.
@@ -41,7 +47,7 @@ constexpr uint32_t kPast = 0x80000000u;   // past every descriptor's range (< 2^
 // Two stages of large steps: a step's requests go out before the step ahead of it is multiplied
 // and are waited for after it.
 template <typename Issue, typename Compute>
-__device__ __forceinline__ void k_loop2(int n, unsigned char* a, unsigned char* b, Issue&& issue, Compute&& compute) {
+__device__ __forceinline__ void k_loop2(int n, Stage a, Stage b, Issue&& issue, Compute&& compute) {
   issue(a, 0);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
@@ -65,7 +71,7 @@ __device__ __forceinline__ void k_loop2(int n, unsigned char* a, unsigned char* 
 // step ahead, during the products, measured 2-6% slower; six stages, which leave a CU one
 // workgroup instead of two, 1-20% slower than four.)
 template <int NST, int L, typename Frag, typename Issue, typename Read, typename Mma>
-__device__ __forceinline__ void k_ring(int n, unsigned char* const (&S)[4], Issue&& issue, Read&& read, Mma&& mma) {
+__device__ __forceinline__ void k_ring(int n, const Stage (&S)[4], Issue&& issue, Read&& read, Mma&& mma) {
   static_assert(NST >= 3 && NST <= 4 && L * (NST - 2) <= 63, "stages and requests per step");
   auto bar = [] {
     asm volatile("" ::: "memory");
@@ -319,9 +325,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
   static_assert(NA >= 1 && NB >= 1 && BM % (RPG * NW) == 0 && BN % (8 * NW) == 0, "load groups per wave");
   static_assert(!SP || BM == 16 * NW, "positions: 16 rows a wave, 4 bytes a lane");
   static_assert(!GLU || FI % 2 == 0, "GLU: gate and up blocks in one wave");
-  constexpr int ST_BYTES = A_BYTES + B_BYTES;   // a stage: weight rows, positions, X rows
-  __shared__ __align__(16) unsigned char s0[ST_BYTES], s1[ST_BYTES], s2[NST > 2 ? ST_BYTES : 16], s3[NST > 3 ? ST_BYTES : 16];
-  unsigned char* const S[4] = {s0, s1, s2, s3};
+  constexpr int A2 = NST > 2 ? A_BYTES : 16, B2 = NST > 2 ? B_BYTES : 16, A3 = NST > 3 ? A_BYTES : 16, B3 = NST > 3 ? B_BYTES : 16;
+  __shared__ __align__(16) unsigned char sA0[A_BYTES], sB0[B_BYTES], sA1[A_BYTES], sB1[B_BYTES], sA2[A2], sB2[B2], sA3[A3],
+      sB3[B3];
+  const Stage S[4] = {{sA0, sB0}, {sA1, sB1}, {sA2, sB2}, {sA3, sB3}};
   __shared__ __align__(16) float sw[2 * BO];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -389,8 +396,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
 #pragma unroll
     for (int j = 0; j < FJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
-  auto issue = [&](unsigned char* a, int si) {
-    unsigned char* const b = a + A_BYTES;
+  auto issue = [&](Stage st, int si) {
+    unsigned char *const a = st.a, *const b = st.b;
     const int s = sb + si;
     const uint32_t at = s == steps_all - 1 ? atail : 0u, bt = s == steps_all - 1 ? btail : 0u;
 #pragma unroll
@@ -411,8 +418,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
   };
   // 256-row tiles (dense): an A fragment a row block ahead, the second half's B fragments during
   // the first
-  auto compute = [&](const unsigned char* a) {
-    const unsigned char* const b = a + A_BYTES;
+  auto compute = [&](Stage st) {
+    const unsigned char *const a = st.a, *const b = st.b;
     auto read_a = [&](int ks, int i) {
       const int r = wmi * SM + i * 16 + fr;
       return *reinterpret_cast<const i32x4*>(a + r * 128 + 16 * swz8(r, 4 * ks + fq));
@@ -452,7 +459,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
     i32x4 a[KS][FI], b0[FJ], b1[FJ];
     int idx[SP ? FI : 1];
   };
-  auto read = [&](Frag& f, const unsigned char* a) {
+  auto read = [&](Frag& f, Stage st) {
+    const unsigned char *const a = st.a, *const b = st.b;
 #pragma unroll
     for (int i = 0; i < FI; ++i) {
       const int r = wmi * SM + i * 16 + fr;
@@ -463,8 +471,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
     }
 #pragma unroll
     for (int j = 0; j < FJ; ++j) {
-      f.b0[j] = read_b(a + A_BYTES, 0, j);
-      f.b1[j] = read_b(a + A_BYTES, 1, j);
+      f.b0[j] = read_b(b, 0, j);
+      f.b1[j] = read_b(b, 1, j);
     }
   };
   auto mma = [&](const Frag& f) {
@@ -490,15 +498,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
   if (n > 0) {
     if constexpr (NST == 2) {
       static_assert(!SP, "2:4 products of this size: k_i8_big");
-      k_loop2(n, s0, s1, issue, compute);
+      k_loop2(n, S[0], S[1], issue, compute);
     } else {
       k_ring<NST, NA + NB + (SP ? 1 : 0), Frag>(n, S, issue, read, mma);
     }
   }
 
-  constexpr int TURN = (GLU ? FI / 2 : FI) % 4 != 0 ? 0 : ST_BYTES >= NW * 8192 ? 8192 : ST_BYTES >= NW * 4096 ? 4096 : 0;
+  constexpr int TURN = (GLU ? FI / 2 : FI) % 4 == 0 && B_BYTES >= NW * 4096 ? 4096 : 0;
   const int ow = GLU ? wmi * SM / 2 : wmi * SM;
-  i8_finish<FI, FJ, GLU, TURN>(acc, epi, part, kpart, T, O, o0 + ow, t0 + wni * SN, lane, s0 + wave * TURN, sw, BO, ow);
+  i8_finish<FI, FJ, GLU, TURN>(acc, epi, part, kpart, T, O, o0 + ow, t0 + wni * SN, lane, sB0 + wave * TURN, sw, BO, ow);
 }
 
 // ----------------------------------------------------------- the large 2:4 products ---
