@@ -214,11 +214,16 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_quant_i8(
 template <bool WAVE, int UN, int SEL, int NK, int LIFT>
 hipError_t launch_q(int threads, const uint16_t* x, int64_t rows, int64_t k, int64_t ldx, int n, int ns, int8_t* q,
                     int64_t ldq, float* scale, hipStream_t s) {
-  const int64_t blocks = WAVE ? (rows + 3) / 4 : rows;
   const size_t lds = LIFT == 1 ? (size_t)((k + 15) / 16 * 16) * (WAVE ? 4 : 1) : 0;
-  k_quant_i8<WAVE, UN, SEL, NK, LIFT><<<dim3((unsigned)blocks), dim3(WAVE ? 256 : threads), lds, s>>>(
-      x, rows, (int)k, ldx, n, ns, q, ldq, scale);
-  return hipGetLastError();
+  constexpr int64_t kRows = (1 << 22) - 4;   // of a launch: a grid holds under 2^32 threads
+  for (int64_t r = 0; r < rows; r += kRows) {
+    const int64_t part = rows - r < kRows ? rows - r : kRows;
+    k_quant_i8<WAVE, UN, SEL, NK, LIFT><<<dim3((unsigned)(WAVE ? (part + 3) / 4 : part)), dim3(WAVE ? 256 : threads), lds, s>>>(
+        x + r * ldx, part, (int)k, ldx, n, ns, q + r * ldq, ldq, scale + r);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // A row per wave up to 2048 values (4 pieces a lane); longer rows 2 pieces a thread up to 4096 values

@@ -107,6 +107,21 @@ def test_quant_borders_and_ranges():
     check_quant(sub | np.where(np.arange(128) % 2, 0x8000, 0).astype(np.uint16))
 
 
+def test_quant_more_rows_than_one_launch_takes():
+    k, distinct, rows = 8, 61, (1 << 22) + 5
+    x = synth.normal_bf16(np.random.default_rng(k), (distinct, k))
+    rq, rs = O.quantize_rows_i8(x)
+    pick = torch.arange(rows, device="cuda") % distinct
+    xd = dev(x)[pick]
+    q = torch.full((rows, up(k, 16)), 77, dtype=torch.int8, device="cuda")
+    s = torch.zeros(rows, device="cuda")
+    S.nm_quant_i8(xd, q, s, k=k)
+    sync()
+    wq = torch.zeros(distinct, up(k, 16), dtype=torch.int8, device="cuda")
+    wq[:, :k] = torch.from_numpy(rq).cuda()
+    assert torch.equal(q, wq[pick]) and torch.equal(s, dev(rs)[pick])
+
+
 def test_quant_zero_and_nonfinite_rows():
     rng = np.random.default_rng(3)
     for k in (64, 4096, 16384):
