@@ -50,17 +50,17 @@ enum class Kind { kFew, kMid, kLarge };
 
 // Up to 32 tokens the streaming kernel, whose row blocks need no partial sums, unless 64 x 32
 // tiles fill the chip unsplit (192 of them) or X, which every row block of the streaming kernel
-// reads again, is long.  Measured (us, streaming / tiles): dense 1 x 4096 x 4096 5.3 / 7.7,
-// 16 x 4096 x 4096 6.7 / 8.2, 32 x 4096 x 4096 8.9 / 9.1, 8 x 4096 x 14336 13.3 / 14.3,
-// 16 x 4096 x 14336 15.7 / 14.7, 32 x 4096 x 14336 22.0 / 15.1, 1 x 14336 x 4096 12.5 / 11.7,
-// 16 x 14336 x 4096 14.4 / 12.6; 2:4 1 x 4096 x 14336 9.8 / 11.4, 16 x 4096 x 14336 14.4 /
-// 12.2, 16 x 14336 x 4096 11.6 / 9.8.  Above, 256 x 256 tiles from 160 of them (dense) or 96 (2:4,
-// whose large kernel is the faster one), smaller tiles below.  Measured (us, smaller / 256 x
-// 256, tiles): dense 2048 x 4096 x 4096 53 / 60 (128), 2048 x 4096 x 14336 127 / 194 (128), 700 x
-// 14336 x 1024 43 / 22 (168), 3000 x 4096 x 2048 55 / 35 (192), GLU 1536 x 4096 x 14336 203 / 222
-// (192), 512 x 14336 x 4096 86 / 65 (224); 2:4 256 x 14336 x 4096 25 / 33 (56), 1536 x 4096 x 14336 95 /
-// 91 (96), 512 x 14336 x 4096 43 / 35 (112), GLU 256 x 14336 x 4096 37 / 36 (112).
-Kind plan_i8(int64_t t, int64_t o, int64_t k, bool sparse, bool glu, uint32_t route) {
+// reads again, is long.  Measured (us, streaming / tiles): dense 1 x 4096 x 4096 5.3 / 7.3,
+// 16 x 4096 x 4096 6.7 / 8.2, 32 x 4096 x 4096 8.8 / 9.0, 8 x 4096 x 14336 13.3 / 14.2,
+// 16 x 4096 x 14336 15.6 / 14.6, 32 x 4096 x 14336 22.0 / 15.1, 1 x 14336 x 4096 12.5 / 10.8,
+// 16 x 14336 x 4096 14.4 / 11.5; 2:4 1 x 4096 x 14336 9.7 / 11.5, 16 x 4096 x 14336 14.4 / 12.2,
+// 16 x 14336 x 4096 11.6 / 8.7.  Above, 256 x 256 tiles from 160 of them, smaller tiles below.
+// Measured (us, smaller / 256 x 256; tiles): dense 2048 x 4096 x 4096 40 / 48 (128), 2048 x 4096 x
+// 14336 112 / 145 (128), 700 x 14336 x 1024 24 / 19 (168), 3000 x 4096 x 2048 35 / 29 (192), GLU
+// 1536 x 4096 x 14336 196 / 162 (192), 1024 x 14336 x 4096 74 / 52 (224); 2:4 512 x 14336 x 4096
+// 31 / 35 (112), 2048 x 4096 x 4096 32 / 34 (128), 2048 x 4096 x 14336 94 / 91 (128), 700 x 14336 x
+// 1024 20 / 18 (168), GLU 256 x 14336 x 4096 30 / 35 (112), 512 x 14336 x 4096 56 / 42 (224).
+Kind plan_i8(int64_t t, int64_t o, int64_t k, bool glu, uint32_t route) {
   if (route & NM_ROUTE_FEW_STREAM) return Kind::kFew;
   if (route & NM_ROUTE_FEW_TILE) return Kind::kMid;
   if (route & NM_ROUTE_TILE_LDS) return Kind::kLarge;
@@ -69,12 +69,12 @@ Kind plan_i8(int64_t t, int64_t o, int64_t k, bool sparse, bool glu, uint32_t ro
     return (o + bo - 1) / bo >= 192 || (t > 8 && t * k > 16 * 8192) ? Kind::kMid : Kind::kFew;
   }
   const int64_t bo = glu ? 128 : 256;
-  return ((o + bo - 1) / bo) * ((t + 255) / 256) >= (sparse ? 96 : 160) ? Kind::kLarge : Kind::kMid;
+  return ((o + bo - 1) / bo) * ((t + 255) / 256) >= 160 ? Kind::kLarge : Kind::kMid;
 }
 
 nm_status run_i8(const nml::I8Args& a, void* ws, int64_t ws_bytes, hipStream_t s) {
   if (a.t == 0 || a.o == 0) return NM_OK;
-  const Kind kind = plan_i8(a.t, a.o, a.k, a.meta != nullptr, a.glu != 0, a.route.flags);
+  const Kind kind = plan_i8(a.t, a.o, a.k, a.glu != 0, a.route.flags);
   int32_t* part = static_cast<int32_t*>(ws);
   if (kind == Kind::kFew || !nml::i8_tile_eligible(a)) return hip_status(nml::launch_i8_few(a, part, ws_bytes, s));
   return hip_status(nml::launch_i8_tile(a, kind == Kind::kLarge, part, ws_bytes, s));
@@ -151,7 +151,7 @@ nm_status nm_glu_i8(const int8_t* x, int64_t t, int64_t k, int64_t ldx, const fl
 
 int64_t nm_i8_workspace_size(int64_t t, int64_t o, int64_t k, int sparse, int glu, uint32_t route) {
   if (t <= 0 || o <= 0 || k <= 0 || k > NM_I8_MAX_K || !span_ok(t, o)) return 0;
-  const Kind kind = plan_i8(t, o, k, sparse != 0, glu != 0, route);
+  const Kind kind = plan_i8(t, o, k, glu != 0, route);
   if (kind == Kind::kLarge) return 0;
   return kind == Kind::kFew ? nml::i8_few_part_bytes(t, o, k, sparse != 0, glu != 0)
                             : nml::i8_mid_part_bytes(t, o, k, glu != 0);

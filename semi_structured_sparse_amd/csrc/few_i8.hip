@@ -248,6 +248,11 @@ struct FewPlan {
   int64_t splits;
 };
 
+// Row blocks of a workgroup: every workgroup reads all of X again, so as many as leave 200
+// workgroups (four blocks against one at 8 x 14336 x 4096: 16.1 -> 11.4 us; a GLU has two
+// weights in a block already).  Waves: few workgroups take more of them, to keep as many loads
+// in flight per CU (16 up to 128 workgroups, 8 up to 512, 4 beyond), at least two steps each.
+// Splits: where under 128 workgroups remain, up to one per CU, four steps a wave at least.
 FewPlan few_plan(int64_t t, int64_t o, int64_t k, bool sparse, bool glu) {
   FewPlan p;
   p.tb = t <= 16 ? 1 : t <= 32 ? 2 : 4;
@@ -285,10 +290,10 @@ hipError_t few_launch(const I8Args& a, const FewPlan& pl, int32_t* part, hipStre
 
 template <int TB, bool SP, bool GLU>
 hipError_t few_rows(const I8Args& a, const FewPlan& pl, int32_t* part, hipStream_t s) {
-  if constexpr (TB <= 2) {
-    if constexpr (!GLU) {
-      if (pl.rw == 4) return few_launch<TB, 4, SP, GLU>(a, pl, part, s);
-    }
+  if constexpr (TB == 1 && !GLU) {
+    if (pl.rw == 4) return few_launch<TB, 4, SP, GLU>(a, pl, part, s);
+  }
+  if constexpr (TB <= 2 && !GLU) {
     if (pl.rw == 2) return few_launch<TB, 2, SP, GLU>(a, pl, part, s);
   }
   return few_launch<TB, 1, SP, GLU>(a, pl, part, s);

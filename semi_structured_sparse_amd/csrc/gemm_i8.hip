@@ -79,31 +79,31 @@ __device__ __forceinline__ void k_ring(int n, const Stage (&S)[4], Issue&& issue
     asm volatile("" ::: "memory");
   };
 #pragma unroll
-    for (int j = 0; j + 1 < NST; ++j) issue(S[j], j < n ? j : n - 1);
+  for (int j = 0; j + 1 < NST; ++j) issue(S[j], j < n ? j : n - 1);
+  __builtin_amdgcn_s_waitcnt(vm_wait(L * (NST - 2)));
+  bar();
+  auto step = [&](int j, int q) {   // j = q % NST, a constant after unrolling
+    const int ahead = q + NST - 1;
+    issue(S[(j + NST - 1) % NST], ahead < n ? ahead : n - 1);
+    Frag f;
+    read(f, S[j]);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f);
     __builtin_amdgcn_s_waitcnt(vm_wait(L * (NST - 2)));
     bar();
-    auto step = [&](int j, int q) {   // j = q % NST, a constant after unrolling
-      const int ahead = q + NST - 1;
-      issue(S[(j + NST - 1) % NST], ahead < n ? ahead : n - 1);
-      Frag f;
-      read(f, S[j]);
-      __builtin_amdgcn_sched_barrier(0);
-      mma(f);
-      __builtin_amdgcn_s_waitcnt(vm_wait(L * (NST - 2)));
-      bar();
-    };
-    int s = 0;
-    for (; s + NST <= n; s += NST) {
+  };
+  int s = 0;
+  for (; s + NST <= n; s += NST) {
 #pragma unroll
-      for (int j = 0; j < NST; ++j) step(j, s + j);
-    }
+    for (int j = 0; j < NST; ++j) step(j, s + j);
+  }
 #pragma unroll
-    for (int j = 0; j + 1 < NST; ++j) {
-      if (s + j >= n) break;
-      step(j, s + j);
-    }
-    __builtin_amdgcn_s_waitcnt(0);
-    bar();
+  for (int j = 0; j + 1 < NST; ++j) {
+    if (s + j >= n) break;
+    step(j, s + j);
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  bar();
 }
 
 // Two fp32 values as packed bf16, to nearest even.
@@ -133,12 +133,12 @@ __device__ __forceinline__ void load_factors(const I8Epi& epi, int64_t o0, int64
 
 // What a wave does with its finished sums: FI x FJ blocks of 16 x 16, lane (fr, fq) = (lane & 15,
 // lane >> 4) holding rows 4 fq + [0, 4) of each block's row range for token fr.  ob_w, tb_w: the
-// wave's first output and token (ow: that output in the tile).  With a split reduction the sums go to part; otherwise each
-// block column's outputs are scaled, turned through the wave's own TURN bytes of LDS at
-// `mine` (a row of 64 outputs per token, 16-byte piece c of row r at c ^ r) and stored as
-// whole row pieces: 128 bytes of bf16 or 256 of fp32.  TURN = 0, or rows that are not
-// 16-byte aligned: element by element.
-template <int FI, int FJ, bool GLU, int TURN>
+// wave's first output and token; ow: that output in the tile.  With a split reduction the sums
+// go to part, otherwise they are scaled.  TURN (256 x 256 tiles): each block column is turned
+// through the wave's own 4 KiB of LDS at `mine` (a row of 64 outputs per token, 16-byte piece c
+// of row r at c ^ r) and stored as whole row pieces, 128 bytes of bf16 or 256 of fp32; smaller
+// tiles store a lane's four outputs at once.  Rows of y that do not allow it: one by one.
+template <int FI, int FJ, bool GLU, bool TURN>
 __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Epi& epi, int32_t* __restrict__ part,
                                           int kpart, int64_t T, int64_t O, int64_t ob_w, int64_t tb_w, int lane,
                                           unsigned char* mine, const float* sw, int BO, int ow) {
@@ -172,29 +172,29 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
   }
   const bool shifted = !GLU && epi.col_shift != nullptr;
   struct Scales {
-    float w[4], u[4], c[4];
+    f32x4 w, e;   // w_scale, and up_scale (GLU) or col_shift
   };
   auto scales = [&](int i) {   // of the lane's four outputs in block i
-    Scales sc;
-    const int at = ow + 16 * i + 4 * fq;   // in the tile
-    const f32x4 w = *reinterpret_cast<const f32x4*>(sw + at);
-    const f32x4 e = GLU || shifted ? *reinterpret_cast<const f32x4*>(sw + BO + at) : f32x4{0.f, 0.f, 0.f, 0.f};
+    const float* at = sw + ow + 16 * i + 4 * fq;   // in the tile
+    return Scales{*reinterpret_cast<const f32x4*>(at),
+                  GLU || shifted ? *reinterpret_cast<const f32x4*>(at + BO) : f32x4{0.f, 0.f, 0.f, 0.f}};
+  };
+  auto values = [&](const Scales& sc, int i, int j) {
+    f32x4 v;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      sc.w[r] = w[r];
-      sc.u[r] = e[r];
-      sc.c[r] = e[r];
+      const int s0 = acc[GLU ? 2 * i : i][j][r], s1 = GLU ? acc[GLU ? 2 * i + 1 : i][j][r] : 0;
+      if constexpr (GLU) v[r] = i8_value<GLU>(epi, s0, s1, xs[j], sc.w[r], sc.e[r], rb[j], sc.e[r]);
+      else v[r] = ((float)s0 * xs[j]) * sc.w[r];
     }
-    return sc;
+    if (shifted) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] += rb[j] * sc.e[r];
+    }
+    return v;
   };
-  auto value = [&](const Scales& sc, int i, int j, int r) {
-    const int s0 = acc[GLU ? 2 * i : i][j][r], s1 = GLU ? acc[GLU ? 2 * i + 1 : i][j][r] : 0;
-    if (!GLU && !shifted) return ((float)s0 * xs[j]) * sc.w[r];
-    return i8_value<GLU>(epi, s0, s1, xs[j], sc.w[r], sc.u[r], rb[j], sc.c[r]);
-  };
-  if constexpr (TURN > 0) {
-    static_assert(NO % 4 == 0 && TURN >= 4096, "rows of 64 outputs");
-    constexpr int JB = TURN >= 8192 && FJ % 2 == 0 ? 2 : 1;   // block columns turned at a time
+  if constexpr (TURN) {
+    static_assert(NO % 4 == 0, "rows of 64 outputs");
     if (epi.bf16_out && epi.ldy % 8 == 0) {
 #pragma unroll
       for (int h = 0; h < NO / 4; ++h) {
@@ -203,28 +203,24 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[i] = scales(4 * h + i);
 #pragma unroll
-        for (int j0 = 0; j0 < FJ; j0 += JB) {
+        for (int j = 0; j < FJ; ++j) {
 #pragma unroll
-          for (int jj = 0; jj < JB; ++jj)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float v[4];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] = value(sc[i], 4 * h + i, j0 + jj, r);
-              *reinterpret_cast<uint2*>(mine + jj * 2048 + fr * 128 + 16 * ((2 * i + (fq >> 1)) ^ (fr & 7)) + 8 * (fq & 1)) =
-                  make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
-            }
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 v = values(sc[i], 4 * h + i, j);
+            *reinterpret_cast<uint2*>(mine + fr * 128 + 16 * ((2 * i + (fq >> 1)) ^ (fr & 7)) + 8 * (fq & 1)) =
+                make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+          }
           __builtin_amdgcn_wave_barrier();
-          uint4 d[2 * JB];
+          uint4 d[2];
 #pragma unroll
-          for (int p = 0; p < 2 * JB; ++p) {
+          for (int p = 0; p < 2; ++p) {
             const int row = 8 * p + (lane >> 3);
             d[p] = *reinterpret_cast<const uint4*>(mine + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
           }
           __builtin_amdgcn_wave_barrier();
 #pragma unroll
-          for (int p = 0; p < 2 * JB; ++p) {
-            const int64_t t = tb_w + 16 * j0 + 8 * p + (lane >> 3), o = oh + 8 * (lane & 7);
+          for (int p = 0; p < 2; ++p) {
+            const int64_t t = tb_w + 16 * j + 8 * p + (lane >> 3), o = oh + 8 * (lane & 7);
             if (t >= T || o >= O) continue;
             uint16_t* yp = static_cast<uint16_t*>(epi.y) + t * epi.ldy + o;
             if (o + 8 <= O) {
@@ -248,27 +244,21 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[i] = scales(4 * h + i);
 #pragma unroll
-        for (int j0 = 0; j0 < FJ; j0 += JB) {
+        for (int j = 0; j < FJ; ++j) {
 #pragma unroll
-          for (int jj = 0; jj < JB; ++jj)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              f32x4 v;
-#pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] = value(sc[i], 4 * h + i, j0 + jj, r);
-              *reinterpret_cast<f32x4*>(mine + jj * 4096 + fr * 256 + 16 * ((4 * i + fq) ^ fr)) = v;
-            }
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4*>(mine + fr * 256 + 16 * ((4 * i + fq) ^ fr)) = values(sc[i], 4 * h + i, j);
           __builtin_amdgcn_wave_barrier();
-          f32x4 d[4 * JB];
+          f32x4 d[4];
 #pragma unroll
-          for (int p = 0; p < 4 * JB; ++p) {
+          for (int p = 0; p < 4; ++p) {
             const int row = 4 * p + (lane >> 4);
             d[p] = *reinterpret_cast<const f32x4*>(mine + row * 256 + 16 * ((lane & 15) ^ (row & 15)));
           }
           __builtin_amdgcn_wave_barrier();
 #pragma unroll
-          for (int p = 0; p < 4 * JB; ++p) {
-            const int64_t t = tb_w + 16 * j0 + 4 * p + (lane >> 4), o = oh + 4 * (lane & 15);
+          for (int p = 0; p < 4; ++p) {
+            const int64_t t = tb_w + 16 * j + 4 * p + (lane >> 4), o = oh + 4 * (lane & 15);
             if (t >= T || o >= O) continue;
             float* yp = static_cast<float*>(epi.y) + t * epi.ldy + o;
             if (o + 4 <= O) {
@@ -285,23 +275,36 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
       return;
     }
   }
+  const bool quads = epi.ldy % 4 == 0;   // four outputs start on a multiple of their size
 #pragma unroll
   for (int i = 0; i < NO; ++i) {
     const Scales sc = scales(i);
+    const int64_t ob = ob0 + 16 * i;
+    if (ob >= O) continue;
 #pragma unroll
     for (int j = 0; j < FJ; ++j) {
       const int64_t t = tb0 + 16 * j;
       if (t >= T) continue;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t o = ob0 + 16 * i + r;
-        if (o >= O) continue;
-        const float v = value(sc, i, j, r);
-        if (epi.bf16_out) {
-          static_cast<uint16_t*>(epi.y)[t * epi.ldy + o] = bf16_rne(v);
+      f32x4 v = values(sc, i, j);
+      if (epi.bf16_out) {
+        uint16_t* yp = static_cast<uint16_t*>(epi.y) + t * epi.ldy + ob;
+        const uint2 d = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+        if (quads && ob + 4 <= O) {
+          *reinterpret_cast<uint2*>(yp) = d;
         } else {
-          float* p = static_cast<float*>(epi.y) + t * epi.ldy + o;
-          *p = epi.accumulate ? *p + v : v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (ob + r < O) yp[r] = (uint16_t)((r < 2 ? d.x : d.y) >> (16 * (r & 1)));
+        }
+      } else {
+        float* yp = static_cast<float*>(epi.y) + t * epi.ldy + ob;
+        if (quads && ob + 4 <= O) {
+          if (epi.accumulate) v += *reinterpret_cast<const f32x4*>(yp);
+          *reinterpret_cast<f32x4*>(yp) = v;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (ob + r < O) yp[r] = epi.accumulate ? yp[r] + v[r] : v[r];
         }
       }
     }
@@ -367,8 +370,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
       int o = GLU ? (r >> 5) * 16 + (r & 15) : r;
       o = o < orows ? o : orows - 1;
       aoff[q] = (uint32_t)(o * (int)ldw + 16 * c);
-      // the piece is the same for every q: the rows of two loads differ by a multiple of 16 (2:4)
-      // or, at 8 waves, 64, and at 4 waves, 32 rows
+      // one piece for every q: the rows of two loads differ by a multiple of 16, the swizzles' period
       if (q == 0) atail = (SP ? last / 2 + 16 * c >= k / 2 : last + 16 * c >= k) ? kPast : 0u;
     }
 #pragma unroll
@@ -453,7 +455,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
       }
     }
   };
-  // smaller tiles: the operands of a whole step at once, a step ahead (k_ring)
+  // smaller tiles: the operands of a whole step at once (k_ring)
   constexpr int KS = SP ? 1 : 2;
   struct Frag {
     i32x4 a[KS][FI], b0[FJ], b1[FJ];
@@ -504,9 +506,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
     }
   }
 
-  constexpr int TURN = (GLU ? FI / 2 : FI) % 4 == 0 && B_BYTES >= NW * 4096 ? 4096 : 0;
+  constexpr bool TURN = NST == 2;
+  static_assert(!TURN || B_BYTES >= NW * 4096, "4 KiB a wave");
   const int ow = GLU ? wmi * SM / 2 : wmi * SM;
-  i8_finish<FI, FJ, GLU, TURN>(acc, epi, part, kpart, T, O, o0 + ow, t0 + wni * SN, lane, sB0 + wave * TURN, sw, BO, ow);
+  i8_finish<FI, FJ, GLU, TURN>(acc, epi, part, kpart, T, O, o0 + ow, t0 + wni * SN, lane, sB0 + wave * 4096, sw, BO, ow);
 }
 
 // ----------------------------------------------------------- the large 2:4 products ---
@@ -897,15 +900,16 @@ struct MidPlan {
   int64_t splits;
 };
 
-// The largest tile that gives 192 workgroups; with none, the smallest, the reduction cut in
-// ranges of at least two steps up to one workgroup per CU.  A split costs the partial sums and
-// a second kernel (4-5 us at 61 x 4096 x 14336), so it is the last choice, except that 64 x 32
-// tiles pay 0.15 us for each step however little it holds: over 64 steps, 64 x 64 tiles in two
-// ranges.  Measured (us; 128 x 128 / 128 x 64 / 64 x 64 / 64 x 32, split to fill the chip):
-// dense 61 x 4096 x 14336 18.9 / 18.0 / 16.2 / 15.5, 777 x 1025 x 1999 17.0 / 14.0 / 10.7 /
-// 10.6, 128 x 4096 x 4096 17.8 / 13.8 / 11.1 / 9.6, 512 x 4096 x 4096 20.0 / 17.3 / 19.1 / 23.1,
-// 2048^3 19.0 / 22.4 / 23.4 / 27.2; 2:4 333 x 4096 x 6144 19.6 / 19.4 / 22.2 / 22.2,
-// 128 x 4096 x 14336 20.3 / 17.0 / 17.0 / 20.5, 1024 x 4096 x 4096 24.3 / 27.1 / 31.8 / 39.1.
+// The largest tile that gives 192 workgroups (of 128 tokens only above 64); with none, the
+// smallest, the reduction cut in ranges of at least two steps up to one workgroup per CU.  A
+// split costs the partial sums and a second kernel (4-5 us at 61 x 4096 x 14336), so it is the
+// last choice, except that 64 x 32 tiles pay 0.15 us for each step however little it holds:
+// over 64 steps, 64 x 64 tiles in two ranges.  Measured (us; 128 x 128 / 128 x 64 / 64 x 64 /
+// 64 x 32, split to fill the chip): dense 61 x 4096 x 14336 18.6 / 17.8 / 15.9 / 15.3, 777 x 1025 x
+// 1999 16.8 / 13.9 / 9.5 / 10.3, 128 x 4096 x 4096 17.8 / 13.5 / 11.0 / 8.5, 512 x 4096 x 4096
+// 19.1 / 13.4 / 15.6 / 20.1, 2048^3 13.1 / 15.9 / 17.4 / 21.4; 2:4 333 x 4096 x 6144 19.4 / 16.8 /
+// 19.6 / 20.6, 128 x 4096 x 14336 20.2 / 16.7 / 16.9 / 19.4, 1024 x 4096 x 4096 18.2 / 21.8 / 25.9 /
+// 33.2; GLU 64 x 14336 x 4096 26.4 / 25.5 / 29.1 / 33.7, 2:4 17.2 / 15.8 / 16.2 / 20.1.
 MidPlan mid_plan(int64_t t, int64_t o, int64_t k, bool glu) {
   const int64_t steps = (k + 127) / 128;
   const int bm[4] = {128, 128, 64, 64}, bn[4] = {128, 64, 64, 32};
@@ -915,7 +919,7 @@ MidPlan mid_plan(int64_t t, int64_t o, int64_t k, bool glu) {
   };
   MidPlan p{3, 1};
   if (t > 32) {
-    for (int sh = 0; sh < 4; ++sh) {
+    for (int sh = t > 64 ? 0 : 1; sh < 4; ++sh) {
       if (tiles(sh) < 192) continue;
       if (sh == 3 && steps > 64) return {2, 2};
       return {sh, 1};
