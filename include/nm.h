@@ -561,9 +561,11 @@ int64_t nm_spense_outsplit_workspace_size(int64_t t, int64_t k, int64_t o_s, int
  * byte of a row is readable, and the bytes of an X row from k up to the next multiple of
  * 16 are ZERO, as nm_quant_i8 writes them (those of W may hold anything).  Codes span
  * [-128, 127] (nm_quant_i8 writes [-127, 127]).  Reduction lengths up to NM_I8_MAX_K keep
- * every sum inside 32 bits; longer ones return NM_EUNSUPPORTED.
+ * every sum inside 32 bits, and the products take up to NM_I8_MAX_ROWS tokens and outputs;
+ * more return NM_EUNSUPPORTED.
  */
 #define NM_I8_MAX_K 131071
+#define NM_I8_MAX_ROWS 134217728
 
 /*
  * nm_quant_i8 -- rows of bf16 to int8 codes and one scale per row: the activations of a

@@ -26,7 +26,7 @@ __all__ = [
     "nm_spense_outsplit_gemm", "nm_spense_outsplit_workspace_size", "nm_quant_lift", "NM_PTS_DYNAMIC",
     "NM_PTS_STATIC", "NM_PTS_VAR", "nm_sparsify_pts", "nm_weight_sums", "NM_ESCRATCH", "nm_spmm_noalloc",
     "NM_NOALLOC_SCRATCH_BYTES", "nm_quant_i8", "nm_meta_block", "nm_meta_block_bytes", "nm_spmm_i8", "nm_glu_i8",
-    "nm_i8_workspace_size", "NM_I8_MAX_K", "NM_Y_F32", "NM_Y_BF16", "NM_GLU_SILU", "NM_GLU_GELU_TANH",
+    "nm_i8_workspace_size", "NM_I8_MAX_K", "NM_I8_MAX_ROWS", "NM_Y_F32", "NM_Y_BF16", "NM_GLU_SILU", "NM_GLU_GELU_TANH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnmsparse.so")
@@ -40,6 +40,7 @@ NM_SPENSE_LOSS, NM_SPENSE_TAIL = 0, 1
 NM_ACT_DYNAMIC, NM_ACT_COMPRESSED, NM_W_COMPRESSED, NM_W_SLIDE, NM_ACT_MASKED = range(5)
 NM_PTS_DYNAMIC, NM_PTS_STATIC, NM_PTS_VAR = 1, 2, 4
 NM_I8_MAX_K = 131071
+NM_I8_MAX_ROWS = 1 << 27
 NM_Y_F32, NM_Y_BF16 = 0, 1
 NM_GLU_SILU, NM_GLU_GELU_TANH = 0, 1
 

@@ -42,7 +42,7 @@ nm_status check_i8(const nml::I8Args& a, const void* ws, int64_t ws_bytes) {
     if (!aligned16(p)) return NM_EALIGN;
   if (a.k > NM_I8_MAX_K) return NM_EUNSUPPORTED;
   if (a.epi.accumulate && a.epi.bf16_out) return NM_EUNSUPPORTED;
-  if (a.t > 0x7FFFFFFF || a.o > 0x7FFFFFFF) return NM_EUNSUPPORTED;
+  if (a.t > NM_I8_MAX_ROWS || a.o > NM_I8_MAX_ROWS) return NM_EUNSUPPORTED;   // a grid holds under 2^32 threads
   return NM_OK;
 }
 

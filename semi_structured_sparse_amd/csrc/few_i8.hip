@@ -17,12 +17,19 @@
 // sixteen kept codes of positions [32 (l / 16), + 32) of a 128-position step with their 32
 // bits of positions, and from X the bytes [16 (l / 16), + 16) and [64 + 16 (l / 16), + 16).
 // A step's last pieces may lie past the row: those loads go to sixteen zero bytes instead.
+//
+// Measured (weights from HBM, us, launches of a replayed graph included): 1 x 4096 x 4096 5.3-5.8,
+// 8 x 4096 x 14336 13.3 (4.4 TB/s), 2:4 1 x 4096 x 14336 9.7, GLU 1 x 4096 x 14336 19.8 (5.9 TB/s).
+// The bound is the weight stream; one-token calls of 17 MB are mostly a launch and two memory
+// latencies, and from 16 tokens on X, read again by every row block, costs more than W.
 #include "i8_device.h"
 
 namespace {
 
 using namespace nmk;
 using namespace nml;
+
+constexpr int64_t kGridY = 65535;   // workgroups of tokens in the grid's y; more go on in z
 
 // TB: blocks of 16 tokens; RW: blocks of 16 output rows; SP: 2:4 weights; GLU: two weights.
 template <int TB, int RW, bool SP, bool GLU>
@@ -48,7 +55,8 @@ __global__ __launch_bounds__(TB >= 4 ? 512 : 1024) void k_few_i8(
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int fr = lane & 15, fq = lane >> 4;
   const int64_t nob = (O + 16 * RW - 1) / (16 * RW);
-  const int64_t ob = blockIdx.x % nob, t0 = (int64_t)blockIdx.y * 16 * TB;
+  const int64_t ob = blockIdx.x % nob, t0 = (blockIdx.y + (int64_t)blockIdx.z * kGridY) * 16 * TB;
+  if (t0 >= T) return;   // the whole workgroup, in the last of z
   const int split = (int)(blockIdx.x / nob);
   const int steps = (k + C::STEP - 1) / C::STEP;
   const int P = splits * waves, p = split * waves + wave;
@@ -277,9 +285,11 @@ template <int TB, int RW, bool SP, bool GLU>
 hipError_t few_launch(const I8Args& a, const FewPlan& pl, int32_t* part, hipStream_t s) {
   using C = FewCfg<TB, RW, SP, GLU>;
   const int64_t nob = (a.o + 16 * RW - 1) / (16 * RW), gy = (a.t + 16 * TB - 1) / (16 * TB);
-  if (nob * pl.splits > 0x7FFFFFFF || gy > 65535) return hipErrorInvalidConfiguration;
+  const int64_t gz = (gy + kGridY - 1) / kGridY;
+  if (nob * pl.splits * 64 * pl.waves > 0xFFFFFFFFll || gz > 65535) return hipErrorInvalidConfiguration;
   const size_t lds = (size_t)pl.waves * C::NA * TB * 256 * 4;
-  k_few_i8<TB, RW, SP, GLU><<<dim3((unsigned)(nob * pl.splits), (unsigned)gy), dim3(64 * pl.waves), lds, s>>>(
+  k_few_i8<TB, RW, SP, GLU><<<dim3((unsigned)(nob * pl.splits), (unsigned)(gz > 1 ? kGridY : gy), (unsigned)gz), dim3(64 * pl.waves),
+                                lds, s>>>(
       a.x, a.ldx, a.w, a.w_up, a.ldw, a.meta, a.up_meta, a.t, a.o, (int)a.k, a.epi, pl.splits > 1 ? part : nullptr,
       (int)pl.splits);
   a.route.note(NM_TAKEN_FEW_STREAM | (SP ? NM_TAKEN_SPARSE_MMA : 0u));

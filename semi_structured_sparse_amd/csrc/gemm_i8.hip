@@ -312,6 +312,12 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
 }
 
 // BM x BN: weight rows by tokens of a tile (GLU: BM / 2 outputs); WM x WN waves; NST stages.
+// Two stages of 256 x 256 (dense): bound by the matrix pipe under the card's power limit.  8192 x
+// 14336 x 4096 379-391 us, 2.5 POPS; the products alone on the same codes take 281 us (on constant
+// ones 238: the clock falls with the bits that change).  GLU 4096 x 14336 x 4096 383-395 us.
+// Rings of smaller tiles: bound by weights from HBM with few tokens (61 x 4096 x 14336 15.3 us with
+// its reduction, GLU 8 x 14336 x 4096 23-25 us, 4.9 TB/s), by the requests' latency in between
+// (2:4 333 x 4096 x 6144 16.8 us: 48 steps of 0.3 us).
 template <int BM, int BN, int WM, int WN, bool SP, bool GLU, int NST>
 __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
     const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w0, const int8_t* __restrict__ w1, int64_t ldw,
@@ -682,7 +688,8 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
 //    takes the requests of the step after the next two.
 // What bounds it: with no requests and real data 211 us (the matrix pipe alone 165 us: power
 // holds its clock down, the same loop on constant operands takes 132), the requests' LDS
-// writes and L2 latency 60 us, epilogue 30 us.
+// writes and L2 latency 60 us, epilogue 30 us.  LDS itself is not full: reading the positions
+// without their two-way bank conflicts (29% of its active cycles) changes nothing.
 template <bool GLU>
 __global__ __launch_bounds__(256) void k_i8_big(
     const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w0, const int8_t* __restrict__ w1, int64_t ldw,

@@ -102,6 +102,8 @@ def test_product_refusals(call, weight):
     assert call(workspace=MIS, workspace_bytes=64) == S.NM_EALIGN
     big = S.NM_I8_MAX_K + 1
     assert call(k=big, ldx=big, ldw=big) == S.NM_EUNSUPPORTED
+    assert call(t=S.NM_I8_MAX_ROWS + 1) == S.NM_EUNSUPPORTED
+    assert call(**{o: S.NM_I8_MAX_ROWS + 1, "ldy": 1 << 31, "t": 1}) == S.NM_EUNSUPPORTED
     assert call(t=1 << 31) == S.NM_EUNSUPPORTED
     assert call(**{o: 1 << 31, "ldy": 1 << 31, "t": 1}) == S.NM_EUNSUPPORTED
 

@@ -574,3 +574,102 @@ def test_binding_refuses_what_does_not_fit():
                 lambda: S.nm_glu_i8(q, s, q, s, torch.zeros(4, 128, dtype=torch.int8, device="cuda"), s, y)):
         with pytest.raises(ValueError):
             bad()
+
+
+def far_rows(rows, ld, dtype, cols, host_rows):
+    """rows x ld with the first columns set, the rest as the allocator left them."""
+    a = torch.empty(rows, ld, dtype=dtype, device="cuda")
+    a[:, :cols] = torch.from_numpy(host_rows).cuda().to(dtype)
+    return a
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_offsets_past_32_bits(sparse):
+    """Rows of X, W and y that start more than 2^32 bytes into their tensors, on every route, and
+    an X whose leading dimension only the streaming kernel takes."""
+    rng = np.random.default_rng(93 + sparse)
+    k = 128
+    for t, o, ldx, ldw, ldy, routes in [(4200, 300, 1 << 20, 256, 304, ("auto", "stream", "split", "tile")),
+                                        (4200, 300, 256, 256, 1 << 18, ("auto", "stream", "split", "tile")),
+                                        (40, 4200, 256, 1 << 20, 4200, ("auto", "stream", "split", "tile")),
+                                        (520, 70, 1 << 23, 256, 70, ("auto",))]:
+        print("far", t, o, ldx, ldw, ldy, flush=True)
+        xc = random_codes(rng, t, k, k, True)
+        _, meta, sc, wv = make_weight(rng, o, k, sparse)
+        wk = k // 2 if sparse else k
+        wc = rng.integers(-128, 128, (o, wk)).astype(np.int8)
+        if sparse:
+            idx = np.sort(rng.random((o, k // 4, 4)).argsort(2)[:, :, :2], axis=2).reshape(o, k // 2).astype(np.uint8)
+            S.nm_meta_block(dev(O.pack_meta_2bit(idx)), o, k, meta)
+            wv = O.expand_24(wc, idx, k)
+        else:
+            wv = wc
+        want = O.sums_i8(xc, wv).astype(np.float64)      # exact in fp32: |sum| <= 2^21
+        x, w = far_rows(t, ldx, torch.int8, k, xc), far_rows(o, ldw, torch.int8, wk, wc)
+        y = torch.empty(t, ldy, device="cuda")
+        one_t, one_o = torch.ones(t, device="cuda"), torch.ones(o, device="cuda")
+        for r in routes:
+            y[:, :o] = float("nan")
+            S.nm_spmm_i8(x, one_t, w, one_o, y, meta, t=t, o=o, k=k, route=ROUTES[r],
+                         workspace=ws_for(t, o, k, sparse, False, ROUTES[r]))
+            sync()
+            assert np.array_equal(y[:, :o].cpu().numpy().astype(np.float64), want), r
+        del x, w, y
+        torch.cuda.empty_cache()
+
+
+def test_quant_offsets_past_32_bits():
+    k, rows, ld = 100, 4200, 1 << 20
+    xb = synth.normal_bf16(np.random.default_rng(95), (rows, k))
+    x = torch.empty(rows, ld, dtype=torch.int16, device="cuda")
+    x[:, :k] = dev(xb)
+    q = torch.empty(rows, ld, dtype=torch.int8, device="cuda")
+    s = torch.empty(rows, device="cuda")
+    S.nm_quant_i8(x, q, s, k=k)
+    sync()
+    rq, rs = O.quantize_rows_i8(xb)
+    assert np.array_equal(q[:, :112].cpu().numpy(), np.pad(rq, ((0, 0), (0, 12)))) and np.array_equal(s.cpu().numpy(), rs)
+
+
+def test_more_token_blocks_than_a_grid_dimension():
+    t, o, k = 65535 * 64 + 70, 3, 16
+    g = torch.Generator(device="cuda").manual_seed(96)
+    x = torch.randint(-128, 128, (t, k), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-128, 128, (o, k), generator=g, device="cuda", dtype=torch.int8)
+    y = torch.full((t + 1, 4), 7.25, device="cuda")
+    for r in ROUTES:
+        y[:t, :o] = float("nan")
+        S.nm_spmm_i8(x, torch.ones(t, device="cuda"), w, torch.ones(o, device="cuda"), y, t=t, o=o, k=k, route=ROUTES[r])
+        sync()
+        want = torch.stack([(x.to(torch.int32) * w[i].to(torch.int32)).sum(1).float() for i in range(o)], 1)
+        assert torch.equal(y[:t, :o], want), r
+        assert (y[t] == 7.25).all() and (y[:, o:] == 7.25).all()
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured products with split reductions and one workspace, replayed in turn."""
+    rng = np.random.default_rng(97)
+    t, o, k = 20, 256, 16384
+    assert S.nm_i8_workspace_size(t, o, k, False, False, 0) > 0
+    ws = ws_for(t, o, k, False, False)
+    calls = []
+    for _ in range(2):
+        x = torch.from_numpy(random_codes(rng, t, k, k, True)).cuda()
+        wd, _, sc, _ = make_weight(rng, o, k, False)
+        calls.append((x, torch.ones(t, device="cuda"), wd, dev(sc), torch.empty(t, o, device="cuda")))
+    want, graphs = [], []
+    for c in calls:
+        S.nm_spmm_i8(*c, workspace=ws)
+        sync()
+        want.append(c[4].clone())
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            S.nm_spmm_i8(*c, workspace=ws)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0):
+        calls[i][4].fill_(float("nan"))
+        graphs[i].replay()
+        sync()
+        assert torch.equal(calls[i][4], want[i])
+        torch.randn(100, device="cuda").sum().item()
