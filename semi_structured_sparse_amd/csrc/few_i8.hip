@@ -260,7 +260,9 @@ struct FewPlan {
 // workgroups (four blocks against one at 8 x 14336 x 4096: 16.1 -> 11.4 us; a GLU has two
 // weights in a block already).  Waves: few workgroups take more of them, to keep as many loads
 // in flight per CU (16 up to 128 workgroups, 8 up to 512, 4 beyond), at least two steps each.
-// Splits: where under 128 workgroups remain, up to one per CU, four steps a wave at least.
+// Splits: where under 128 workgroups remain, up to one per CU, four steps a wave at least, and
+// only where a wave has over eight weight pieces unsplit (1 x 512 x 8192, eight of them: 6.7 us
+// either way, and outside a graph a launch more; x 11008 8.5 unsplit, 7.9 in two).
 FewPlan few_plan(int64_t t, int64_t o, int64_t k, bool sparse, bool glu) {
   FewPlan p;
   p.tb = t <= 16 ? 1 : t <= 32 ? 2 : 4;
@@ -277,6 +279,7 @@ FewPlan few_plan(int64_t t, int64_t o, int64_t k, bool sparse, bool glu) {
   int64_t s = blocks > 0 ? 256 / blocks : 1;
   const int64_t room = steps / (4 * p.waves);
   if (s > room) s = room;
+  if (steps * mats <= 8 * p.waves) s = 1;
   p.splits = s < 2 ? 1 : s > 16 ? 16 : s;
   return p;
 }

@@ -908,10 +908,12 @@ struct MidPlan {
 };
 
 // The largest tile that gives 192 workgroups (of 128 tokens only above 64); with none, the
-// smallest, the reduction cut in ranges of at least two steps up to one workgroup per CU.  A
-// split costs the partial sums and a second kernel (4-5 us at 61 x 4096 x 14336), so it is the
-// last choice, except that 64 x 32 tiles pay 0.15 us for each step however little it holds:
-// over 64 steps, 64 x 64 tiles in two ranges.  Measured (us; 128 x 128 / 128 x 64 / 64 x 64 /
+// smallest, a reduction of over 32 steps cut in ranges of at least 16 up to one workgroup per
+// CU.  A split costs the partial sums and a second kernel, 3-5 us against 0.13-0.15 us for each step
+// (100 x 500 x 2048 unsplit 5.0, in 8 ranges 7.7; x 8192 12.3 unsplit, 7.8 in 4, 8.4 in 8; 40 x
+// 256 x 14336 17.4 unsplit, 8.4 in 7, 9.3 in 14, 12.5 in 32), so it is the last choice, except
+// that 64 x 32 tiles pay for each step however little it holds: over 64 steps, 64 x 64 tiles in
+// two ranges.  Measured (us; 128 x 128 / 128 x 64 / 64 x 64 /
 // 64 x 32, split to fill the chip): dense 61 x 4096 x 14336 18.6 / 17.8 / 15.9 / 15.3, 777 x 1025 x
 // 1999 16.8 / 13.9 / 9.5 / 10.3, 128 x 4096 x 4096 17.8 / 13.5 / 11.0 / 8.5, 512 x 4096 x 4096
 // 19.1 / 13.4 / 15.6 / 20.1, 2048^3 13.1 / 15.9 / 17.4 / 21.4; 2:4 333 x 4096 x 6144 19.4 / 16.8 /
@@ -933,8 +935,8 @@ MidPlan mid_plan(int64_t t, int64_t o, int64_t k, bool glu) {
     }
   }
   p.splits = tiles(3) > 0 ? 256 / tiles(3) : 1;
-  if (p.splits > steps / 2) p.splits = steps / 2;
-  if (p.splits < 1) p.splits = 1;
+  if (p.splits > steps / 16) p.splits = steps / 16;
+  if (steps <= 32 || p.splits < 1) p.splits = 1;
   return p;
 }
 
