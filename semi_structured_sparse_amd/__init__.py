@@ -536,9 +536,24 @@ def _factors(t, n, dev):
     return t.data_ptr()
 
 
-def _i8_out(y):
-    """NM_Y_* of an output tensor (raw pointers: fp32)."""
-    return NM_Y_BF16 if y is not None and type(y) is not int and y.element_size() == 2 else NM_Y_F32
+def _i8_out(y, t, o, dev):
+    """(pointer, leading dimension, NM_Y_*) of an output of at least t rows of o (raw pointers: fp32)."""
+    p, ld = _mat(y, dev)
+    if y is None or type(y) is int:
+        return p, ld, NM_Y_F32
+    size, shape = y.element_size(), y.shape
+    if (size != 4 and size != 2) or shape[0] < t or shape[1] < o:
+        raise ValueError(f"y of {t} rows of {o} fp32 or bf16 values is needed")
+    return p, ld, NM_Y_F32 if size == 4 else NM_Y_BF16
+
+
+def _meta(t, o, k, dev):
+    """Pointer of blocked positions (nm_meta_block) of at least o rows over k."""
+    if t is None or type(t) is int:
+        return t
+    if t.get_device() != dev or t.numel() * t.element_size() < (k + 127) // 128 * o * 16 or not t.is_contiguous():
+        _refuse(t, dev, "contiguous blocked positions of all rows are needed")
+    return t.data_ptr()
 
 
 def _bytes(t):
@@ -554,6 +569,8 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
         rows = x.shape[0]
     if k is None:
         k = x.shape[1]
+    if q is not None and type(q) is not int and q.shape[0] < rows:
+        raise ValueError(f"q of {rows} rows is needed")
     st = lib().nm_quant_i8(xp, rows, k, lx if ldx is None else ldx, n, m, ns, qp, lq if ldq is None else ldq,
                            _factors(scale, rows, dev), _stream(stream))
     if check and st:
@@ -586,17 +603,17 @@ def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift
     dev = _device() if stream is None else _device_of(x, w, y)
     xp, lx = _mat(x, dev, 1)
     wp, lw = _mat(w, dev, 1)
-    yp, ly = _mat(y, dev)
     if t is None:
         t = x.shape[0]
     if o is None:
         o = w.shape[0]
     if k is None:
         k = x.shape[1]
+    yp, ly, yd = _i8_out(y, t, o, dev)
     st = lib().nm_spmm_i8(xp, t, k, lx if ldx is None else ldx, _factors(x_scale, t, dev), wp, o,
-                          lw if ldw is None else ldw, _factors(w_scale, o, dev), _vec(w_meta, dev),
+                          lw if ldw is None else ldw, _factors(w_scale, o, dev), _meta(w_meta, o, k, dev),
                           _factors(row_shift, t, dev), _factors(col_shift, o, dev), yp,
-                          ly if ldy is None else ldy, _i8_out(y) if y_dtype is None else y_dtype, accumulate,
+                          ly if ldy is None else ldy, yd if y_dtype is None else y_dtype, accumulate,
                           _vec(workspace, dev), _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
                           ctypes.addressof(taken) if taken is not None else None, _stream(stream))
     if check and st:
@@ -613,7 +630,6 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
     xp, lx = _mat(x, dev, 1)
     gp, lg = _mat(w_gate, dev, 1)
     up, lu = _mat(w_up, dev, 1)
-    yp, ly = _mat(y, dev)
     if ldw is None:
         if lg != lu:
             raise ValueError("w_gate and w_up need the same leading dimension")
@@ -622,12 +638,15 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
         t = x.shape[0]
     if inter is None:
         inter = w_gate.shape[0]
+        if type(w_up) is not int and w_up.shape[0] != inter:
+            raise ValueError("w_gate and w_up need the same rows")
     if k is None:
         k = x.shape[1]
+    yp, ly, yd = _i8_out(y, t, inter, dev)
     st = lib().nm_glu_i8(xp, t, k, lx if ldx is None else ldx, _factors(x_scale, t, dev), gp,
-                         _factors(gate_scale, inter, dev), _vec(gate_meta, dev), up,
-                         _factors(up_scale, inter, dev), _vec(up_meta, dev), inter, ldw, act, yp,
-                         ly if ldy is None else ldy, _i8_out(y) if y_dtype is None else y_dtype, _vec(workspace, dev),
+                         _factors(gate_scale, inter, dev), _meta(gate_meta, inter, k, dev), up,
+                         _factors(up_scale, inter, dev), _meta(up_meta, inter, k, dev), inter, ldw, act, yp,
+                         ly if ldy is None else ldy, yd if y_dtype is None else y_dtype, _vec(workspace, dev),
                          _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
                          ctypes.addressof(taken) if taken is not None else None, _stream(stream))
     if check and st:

@@ -569,7 +569,10 @@ def test_binding_refuses_what_does_not_fit():
                 lambda: S.nm_quant_i8(x, q, s[:3]), lambda: S.nm_quant_i8(x, q, s.double()),
                 lambda: S.nm_quant_i8(x, q.cpu(), s), lambda: S.nm_spmm_i8(q, s[:3], q, s, y),
                 lambda: S.nm_spmm_i8(q, s, q, s[::2], y), lambda: S.nm_spmm_i8(x, s, q, s, y),
-                lambda: S.nm_spmm_i8(q, s, q, s, y.cpu()), lambda: S.nm_spmm_i8(q, s, q, s, y, col_shift=s[:2]),
+                lambda: S.nm_spmm_i8(q, s, q, s, y.to(torch.int8)), lambda: S.nm_spmm_i8(q, s, q, s, y.double()),
+                lambda: S.nm_spmm_i8(q, s, q, s, y[:3]), lambda: S.nm_spmm_i8(q, s, q, s, y[:, :3]),
+                lambda: S.nm_glu_i8(q, s, q, s, q, s, y[:3]), lambda: S.nm_glu_i8(q, s, q, s, q[:3], s, y),
+                lambda: S.nm_quant_i8(x, q[:3], s), lambda: S.nm_spmm_i8(q, s, q, s, y, q[:, :15], k=64), lambda: S.nm_spmm_i8(q, s, q, s, y.cpu()), lambda: S.nm_spmm_i8(q, s, q, s, y, col_shift=s[:2]),
                 lambda: S.nm_spmm_i8(q, s, q, s, y, workspace=q.cpu()), lambda: S.nm_glu_i8(q, s, q, s, q.t(), s, y),
                 lambda: S.nm_glu_i8(q, s, q, s, torch.zeros(4, 128, dtype=torch.int8, device="cuda"), s, y)):
         with pytest.raises(ValueError):
