@@ -244,7 +244,7 @@ hipError_t by_length(const uint16_t* x, int64_t rows, int64_t k, int64_t ldx, in
   return launch_q<false, 8 / PU, SEL, NK, LIFT>(threads, x, rows, k, ldx, n, ns, q, ldq, scale, s);
 }
 
-// A thread per 16 bytes of output (offline, once a weight): block s of row r holds the positions of slots
+// A thread per 16 bytes of output (offline, once a weight: 14336 x 4096 17.7 us): block s of row r holds the positions of slots
 // [64 s, 64 s + 64), bytes past the row filled with the slots 0, 1, 0, 1 (0x44).
 __global__ __launch_bounds__(256) void k_meta_step_block(const uint8_t* __restrict__ meta, int64_t o, int64_t kc,
                                                          int64_t steps, uint8_t* __restrict__ out) {
