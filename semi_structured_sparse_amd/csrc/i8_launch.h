@@ -38,11 +38,12 @@ hipError_t launch_quant_i8(const uint16_t* x, int64_t rows, int64_t k, int64_t l
                            int64_t ldq, float* scale, hipStream_t s);
 hipError_t launch_meta_step_block(const uint8_t* meta, int64_t o, int64_t kc, uint8_t* out, hipStream_t s);
 
-// Streaming kernel: any shape; part (scratch) or null as in launch_i8_product.
+// Streaming kernel: any shape.  The reduction is split across workgroups where part holds
+// i8_few_part_bytes.
 hipError_t launch_i8_few(const I8Args& a, int32_t* part, int64_t part_bytes, hipStream_t s);
 int64_t i8_few_part_bytes(int64_t t, int64_t o, int64_t k, bool sparse, bool glu);
 
-// Tile kernel: 256 x 256 tiles (large), or 128-row tiles with the reduction split across
+// Tile kernels: 256 x 256 tiles (large), or smaller ones by shape, the reduction split across
 // workgroups where part holds i8_mid_part_bytes.
 bool i8_tile_eligible(const I8Args& a);
 int64_t i8_mid_part_bytes(int64_t t, int64_t o, int64_t k, bool glu);

@@ -248,6 +248,22 @@ def test_product_larger_shapes(sparse):
         check_product(rng, t, o, k, sparse, bf16=True, ldy=up(o, 8))
 
 
+SPLIT_SHAPES = [(1, 65, 32768), (8, 501, 32768), (16, 512, 14336), (40, 258, 14336), (61, 1030, 8192), (130, 300, 9000),
+                (200, 1001, 6144)]
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_split_reductions(sparse):
+    """Shapes whose reduction is cut across workgroups, with every epilogue of the summing kernel."""
+    rng = np.random.default_rng(44 + sparse)
+    for t, o, k in SPLIT_SHAPES:
+        assert S.nm_i8_workspace_size(t, o, k, sparse, False) > 0, (t, o, k)
+        check_product(rng, t, o, k, sparse, routes=("auto", "stream", "split"))
+        check_product(rng, t, o, k, sparse, bf16=True, shift=1, ldy=up(o, 8))
+        check_product(rng, t, o, k, sparse, shift=2, accumulate=1, ldy=o + 3)
+        check_product(rng, t, o, k, sparse, shift=2, ldy=up(o, 4), routes=("auto", "tile"))
+
+
 def test_longest_reduction_stays_inside_32_bits():
     """All codes -128: the sum is 128 * 128 * k, the largest that can occur."""
     k = S.NM_I8_MAX_K
@@ -341,6 +357,15 @@ def test_glu(sparse, act):
     for t, o, k in [(1, 2048, 4096), (8, 14336, 256), (600, 1030, 1024), (1100, 1100, 640)]:
         check_glu(rng, t, o, k, sparse, act)
         check_glu(rng, t, o, k, sparse, act, bf16=True)
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_glu_split_reductions(sparse):
+    rng = np.random.default_rng(64 + sparse)
+    for t, o, k in SPLIT_SHAPES[:-2] + [(130, 300, 9000)]:
+        assert S.nm_i8_workspace_size(t, o, k, sparse, True) > 0, (t, o, k)
+        check_glu(rng, t, o, k, sparse, "silu", routes=("auto", "stream", "split"))
+        check_glu(rng, t, o, k, sparse, "gelu", bf16=True, ldy=up(o, 4))
 
 
 def test_glu_far_gates():
