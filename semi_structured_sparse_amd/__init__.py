@@ -196,11 +196,13 @@ def _ld(t, default=0):
 
 _current_raw_stream = None      # () -> raw current stream of the current device
 _current_device = None          # () -> the current device
+_half = None                    # torch.float16, which the int8 layers refuse where bf16 is meant
 
 
 def _bind_torch():
-    global _current_raw_stream, _current_device
+    global _current_raw_stream, _current_device, _half
     import torch
+    _half = torch.float16
     torch.cuda.current_stream()             # initialises the device
     raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
     # building a Stream object costs 2.7 us a call, the raw handle 0.2 us (one-token calls take 6)
@@ -542,7 +544,7 @@ def _i8_out(y, t, o, dev):
     if y is None or type(y) is int:
         return p, ld, NM_Y_F32
     size, shape = y.element_size(), y.shape
-    if (size != 4 and size != 2) or shape[0] < t or shape[1] < o:
+    if (size != 4 and size != 2) or shape[0] < t or shape[1] < o or y.dtype is _half:
         raise ValueError(f"y of {t} rows of {o} fp32 or bf16 values is needed")
     return p, ld, NM_Y_F32 if size == 4 else NM_Y_BF16
 
@@ -569,6 +571,8 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
         rows = x.shape[0]
     if k is None:
         k = x.shape[1]
+    if type(x) is not int and x is not None and x.dtype is _half:
+        raise ValueError("x of bf16 values is needed")
     if q is not None and type(q) is not int and q.shape[0] < rows:
         raise ValueError(f"q of {rows} rows is needed")
     st = lib().nm_quant_i8(xp, rows, k, lx if ldx is None else ldx, n, m, ns, qp, lq if ldq is None else ldq,

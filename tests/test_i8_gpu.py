@@ -590,7 +590,8 @@ def test_binding_refuses_what_does_not_fit():
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
     q, s = torch.zeros(4, 64, dtype=torch.int8, device="cuda"), torch.zeros(4, device="cuda")
     y = torch.zeros(4, 4, device="cuda")
-    for bad in (lambda: S.nm_quant_i8(x.float(), q, s), lambda: S.nm_quant_i8(x, x, s), lambda: S.nm_quant_i8(x.t(), q, s),
+    for bad in (lambda: S.nm_quant_i8(x.half(), q, s), lambda: S.nm_spmm_i8(q, s, q, s, y.half()),
+                lambda: S.nm_quant_i8(x.float(), q, s), lambda: S.nm_quant_i8(x, x, s), lambda: S.nm_quant_i8(x.t(), q, s),
                 lambda: S.nm_quant_i8(x, q, s[:3]), lambda: S.nm_quant_i8(x, q, s.double()),
                 lambda: S.nm_quant_i8(x, q.cpu(), s), lambda: S.nm_spmm_i8(q, s[:3], q, s, y),
                 lambda: S.nm_spmm_i8(q, s, q, s[::2], y), lambda: S.nm_spmm_i8(x, s, q, s, y),
