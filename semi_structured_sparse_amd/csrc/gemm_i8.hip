@@ -66,7 +66,8 @@ __device__ __forceinline__ void k_loop2(int n, Stage a, Stage b, Issue&& issue, 
 }
 
 // Small steps: step q requests step q + NST - 1 into the stage that step q - 1 used, reads its
-// operands, all at once, and multiplies; then one wait (step q + 1 has landed) and one barrier.
+// operands, all at once, and multiplies; then one wait (step q + 1 has landed, the operands have
+// arrived) and one barrier.
 // Past the last step the last one is requested again; no one reads it.  (Reading operands a
 // step ahead, during the products, measured 2-6% slower; six stages, which leave a CU one
 // workgroup instead of two, 1-20% slower than four.)
@@ -89,7 +90,9 @@ __device__ __forceinline__ void k_ring(int n, const Stage (&S)[4], Issue&& issue
     read(f, S[j]);
     __builtin_amdgcn_sched_barrier(0);
     mma(f);
-    __builtin_amdgcn_s_waitcnt(vm_wait(L * (NST - 2)));
+    // the reads too: the compiler may move products, and with them the waits for their operands,
+    // past the barrier, behind which this stage is requested into
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0 & vm_wait(L * (NST - 2)));
     bar();
   };
   int s = 0;

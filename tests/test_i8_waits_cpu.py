@@ -6,6 +6,9 @@ Requests complete in issue order, so a wait before a step may leave at most the 
 issued after that step's: those of the NST - 2 steps behind it.  The loops are replayed and every
 vmcnt wait is held against that count.
 
+A stage is requested into again one barrier after it was read, so at every barrier of a loop all
+LDS reads before it must have been waited for (lgkmcnt(0)).
+
 k_i8_big multiplies in inline assembly on the accumulator half of the register file.  Its loop
 must hold every sum where it is (no move between the register halves, no scratch), and the first
 read of a sum after the loop must lie 19 issue slots (a 16-pass matrix instruction's latency
@@ -38,6 +41,32 @@ def _events(body):
         elif t.startswith(("global_", "buffer_", "flat_", "scratch_")):
             ev.append(("vload",))
     return ev
+
+
+def _reads_at_barriers(body):
+    """LDS reads that no lgkmcnt wait has covered when a barrier is reached, the most of any."""
+    out, most = 0, 0
+    for line in body * 2:
+        t = line.split(";")[0].strip()
+        if t.startswith("ds_read"):
+            out += 1
+        elif t.startswith("s_waitcnt"):
+            m = re.search(r"lgkmcnt\((\d+)\)", t)
+            if m:
+                out = min(out, int(m.group(1)))
+        elif t.startswith("s_barrier"):
+            most = max(most, out)
+    return most
+
+
+def test_reads_are_complete_at_barriers(asm):
+    n = 0
+    for name, body in _functions(asm, "k_i8_tileI") + _functions(asm, "k_i8_bigI"):
+        assert _reads_at_barriers(body) == 0, name
+        for lp in _loops(body):
+            assert _reads_at_barriers(lp) == 0, name
+        n += 1
+    assert n == 20
 
 
 def _rings(body):
