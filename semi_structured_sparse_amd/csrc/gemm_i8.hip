@@ -139,8 +139,11 @@ __device__ __forceinline__ void load_factors(const I8Epi& epi, int64_t o0, int64
 // wave's first output and token; ow: that output in the tile.  With a split reduction the sums
 // go to part, otherwise they are scaled.  TURN (256 x 256 tiles): each block column is turned
 // through the wave's own 4 KiB of LDS at `mine` (a row of 64 outputs per token, 16-byte piece c
-// of row r at c ^ r) and stored as whole row pieces, 128 bytes of bf16 or 256 of fp32; smaller
-// tiles store a lane's four outputs at once.  Rows of y that do not allow it: one by one.
+// of row r at c ^ r) and stored as whole row pieces, 128 bytes of bf16 or 256 of fp32.  Smaller
+// tiles store a lane's four outputs at once.  Where rows of y do not keep that alignment, both
+// turn (smaller tiles in 2 KiB) and neighbouring lanes store neighbouring outputs: stored one by
+// one from where the sums lie, 4096 x 4095 x 2048 took 53 us instead of 34, 777 x 1025 x 2048 8.4
+// instead of 7.8.
 template <int FI, int FJ, bool GLU, bool TURN>
 __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Epi& epi, int32_t* __restrict__ part,
                                           int kpart, int64_t T, int64_t O, int64_t ob_w, int64_t tb_w, int lane,
@@ -198,7 +201,8 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
   };
   if constexpr (TURN) {
     static_assert(NO % 4 == 0, "rows of 64 outputs");
-    if (epi.bf16_out && epi.ldy % 8 == 0) {
+    if (epi.bf16_out) {
+      const bool whole = epi.ldy % 8 == 0;
 #pragma unroll
       for (int h = 0; h < NO / 4; ++h) {
         const int64_t oh = ob_w + 64 * h;
@@ -214,6 +218,17 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
                 make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
           }
           __builtin_amdgcn_wave_barrier();
+          if (!whole) {
+            if (oh + lane < O) {
+              uint16_t* yp = static_cast<uint16_t*>(epi.y) + (tb_w + 16 * j) * epi.ldy + oh + lane;
+              const int rows = (int)(T - tb_w - 16 * j < 16 ? T - tb_w - 16 * j : 16);
+#pragma unroll 8
+              for (int r = 0; r < rows; ++r, yp += epi.ldy)
+                *yp = *reinterpret_cast<const uint16_t*>(mine + r * 128 + 16 * ((lane >> 3) ^ (r & 7)) + 2 * (lane & 7));
+            }
+            __builtin_amdgcn_wave_barrier();
+            continue;
+          }
           uint4 d[2];
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
@@ -239,7 +254,8 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
       }
       return;
     }
-    if (!epi.bf16_out && epi.ldy % 4 == 0) {
+    if (!epi.bf16_out) {
+      const bool whole = epi.ldy % 4 == 0;
 #pragma unroll
       for (int h = 0; h < NO / 4; ++h) {
         const int64_t oh = ob_w + 64 * h;
@@ -252,6 +268,19 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<f32x4*>(mine + fr * 256 + 16 * ((4 * i + fq) ^ fr)) = values(sc[i], 4 * h + i, j);
           __builtin_amdgcn_wave_barrier();
+          if (!whole) {
+            if (oh + lane < O) {
+              float* yp = static_cast<float*>(epi.y) + (tb_w + 16 * j) * epi.ldy + oh + lane;
+              const int rows = (int)(T - tb_w - 16 * j < 16 ? T - tb_w - 16 * j : 16);
+#pragma unroll 8
+              for (int r = 0; r < rows; ++r, yp += epi.ldy) {
+                const float e = *reinterpret_cast<const float*>(mine + r * 256 + 16 * ((lane >> 2) ^ r) + 4 * (lane & 3));
+                *yp = epi.accumulate ? *yp + e : e;
+              }
+            }
+            __builtin_amdgcn_wave_barrier();
+            continue;
+          }
           f32x4 d[4];
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
@@ -278,36 +307,66 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
       return;
     }
   }
-  const bool quads = epi.ldy % 4 == 0;   // four outputs start on a multiple of their size
+  if constexpr (!TURN) {
+    if (epi.ldy % 4 == 0) {   // four outputs start on a multiple of their size
 #pragma unroll
-  for (int i = 0; i < NO; ++i) {
-    const Scales sc = scales(i);
-    const int64_t ob = ob0 + 16 * i;
-    if (ob >= O) continue;
+      for (int i = 0; i < NO; ++i) {
+        const Scales sc = scales(i);
+        const int64_t ob = ob0 + 16 * i;
+        if (ob >= O) continue;
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) {
+          const int64_t t = tb0 + 16 * j;
+          if (t >= T) continue;
+          f32x4 v = values(sc, i, j);
+          if (epi.bf16_out) {
+            uint16_t* yp = static_cast<uint16_t*>(epi.y) + t * epi.ldy + ob;
+            const uint2 d = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+            if (ob + 4 <= O) {
+              *reinterpret_cast<uint2*>(yp) = d;
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (ob + r < O) yp[r] = (uint16_t)((r < 2 ? d.x : d.y) >> (16 * (r & 1)));
+            }
+          } else {
+            float* yp = static_cast<float*>(epi.y) + t * epi.ldy + ob;
+            if (ob + 4 <= O) {
+              if (epi.accumulate) v += *reinterpret_cast<const f32x4*>(yp);
+              *reinterpret_cast<f32x4*>(yp) = v;
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (ob + r < O) yp[r] = epi.accumulate ? yp[r] + v[r] : v[r];
+            }
+          }
+        }
+      }
+      return;
+    }
+    static_assert(NO <= 2, "2 KiB hold 16 tokens of 32 outputs");
+    constexpr int W = 16 * NO;   // outputs of a row
+    auto piece = [](int r, int c) { return r * (4 * W) + 16 * (NO == 2 ? swz8(r, c) : swz4(r, c)); };
+    const int64_t o = ob_w + lane % W;
 #pragma unroll
     for (int j = 0; j < FJ; ++j) {
-      const int64_t t = tb0 + 16 * j;
-      if (t >= T) continue;
-      f32x4 v = values(sc, i, j);
-      if (epi.bf16_out) {
-        uint16_t* yp = static_cast<uint16_t*>(epi.y) + t * epi.ldy + ob;
-        const uint2 d = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
-        if (quads && ob + 4 <= O) {
-          *reinterpret_cast<uint2*>(yp) = d;
-        } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (ob + r < O) yp[r] = (uint16_t)((r < 2 ? d.x : d.y) >> (16 * (r & 1)));
-        }
-      } else {
-        float* yp = static_cast<float*>(epi.y) + t * epi.ldy + ob;
-        if (quads && ob + 4 <= O) {
-          if (epi.accumulate) v += *reinterpret_cast<const f32x4*>(yp);
-          *reinterpret_cast<f32x4*>(yp) = v;
-        } else {
+      for (int i = 0; i < NO; ++i) *reinterpret_cast<f32x4*>(mine + piece(fr, 4 * i + fq)) = values(scales(i), i, j);
+      __builtin_amdgcn_wave_barrier();
+      float e[W / 4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (ob + r < O) yp[r] = epi.accumulate ? yp[r] + v[r] : v[r];
+      for (int p = 0; p < W / 4; ++p)
+        e[p] = *reinterpret_cast<const float*>(mine + piece(64 / W * p + lane / W, lane % W / 4) + 4 * (lane & 3));
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int p = 0; p < W / 4; ++p) {
+        const int64_t t = tb_w + 16 * j + 64 / W * p + lane / W;
+        if (t >= T || o >= O) continue;
+        if (epi.bf16_out) {
+          static_cast<uint16_t*>(epi.y)[t * epi.ldy + o] = (uint16_t)bf16x2(e[p], 0.f);
+        } else {
+          float* yp = static_cast<float*>(epi.y) + t * epi.ldy + o;
+          *yp = epi.accumulate ? *yp + e[p] : e[p];
         }
       }
     }
@@ -516,9 +575,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
   }
 
   constexpr bool TURN = NST == 2;
-  static_assert(!TURN || B_BYTES >= NW * 4096, "4 KiB a wave");
+  static_assert(TURN ? B_BYTES >= NW * 4096 : A_BYTES >= NW / 2 * 2048, "LDS of a wave to turn in");
+  unsigned char* const mine = TURN ? sB0 + wave * 4096 : (wave < NW / 2 ? sA0 : sA1) + wave % (NW / 2) * 2048;
   const int ow = GLU ? wmi * SM / 2 : wmi * SM;
-  i8_finish<FI, FJ, GLU, TURN>(acc, epi, part, kpart, T, O, o0 + ow, t0 + wni * SN, lane, sB0 + wave * 4096, sw, BO, ow);
+  i8_finish<FI, FJ, GLU, TURN>(acc, epi, part, kpart, T, O, o0 + ow, t0 + wni * SN, lane, mine, sw, BO, ow);
 }
 
 // ----------------------------------------------------------- the large 2:4 products ---
@@ -550,7 +610,10 @@ __device__ __forceinline__ int acc_read(int a) {
 // holds, in register v, row 8 (v / 4) + 4 h + v % 4 of token c.  GLU: the rows of a block are 16
 // gate rows and the 16 up rows of the same outputs, registers v and v + 8.  As i8_finish: rows
 // of 64 outputs and 32 tokens are turned in the wave's own 8 KiB of LDS and stored whole.
-template <bool GLU>
+// WHOLE: rows of y keep the alignment (a form of its own: as one, the registers of the other cost
+// aligned outputs 2 us of 28 at 4096 x 4096 x 2048); otherwise neighbouring lanes store
+// neighbouring outputs.
+template <bool GLU, bool WHOLE>
 __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I8Epi& epi, int64_t T, int64_t O,
                                               int64_t ob_w, int64_t tb_w, int lane, unsigned char* mine,
                                               const float* sw, int ow) {
@@ -567,7 +630,6 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
     xs[j] = epi.x_scale[t];
     rb[j] = !GLU && epi.row_shift != nullptr ? epi.row_shift[t] : 1.f;
   }
-  const bool rows16 = epi.bf16_out ? epi.ldy % 8 == 0 : epi.ldy % 4 == 0;
 #pragma unroll
   for (int hh = 0; hh < NH; ++hh) {
     const int64_t oh = ob_w + 64 * hh;
@@ -618,6 +680,17 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
                 make_uint2(bf16x2(v[b][g][0], v[b][g][1]), bf16x2(v[b][g][2], v[b][g][3]));
           }
         __builtin_amdgcn_wave_barrier();
+        if constexpr (!WHOLE) {
+          if (oh + lane < O) {
+            uint16_t* yp = static_cast<uint16_t*>(epi.y) + tj * epi.ldy + oh + lane;
+            const int rows = (int)(T - tj < 32 ? T - tj : 32);
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r, yp += epi.ldy)
+              *yp = *reinterpret_cast<const uint16_t*>(mine + r * 128 + 16 * ((lane >> 3) ^ ((r >> 1) & 7)) + 2 * (lane & 7));
+          }
+          __builtin_amdgcn_wave_barrier();
+          continue;
+        }
         uint4 d[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
@@ -630,7 +703,7 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
           const int64_t t = tj + 8 * p + (lane >> 3), o = oh + 8 * (lane & 7);
           if (t >= T || o >= O) continue;
           uint16_t* yp = static_cast<uint16_t*>(epi.y) + t * epi.ldy + o;
-          if (rows16 && o + 8 <= O) {
+          if (o + 8 <= O) {
             *reinterpret_cast<uint4*>(yp) = d[p];
           } else {
             const uint32_t e[4] = {d[p].x, d[p].y, d[p].z, d[p].w};
@@ -650,6 +723,19 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
                 f32x4{v[b][g][0], v[b][g][1], v[b][g][2], v[b][g][3]};
           }
         __builtin_amdgcn_wave_barrier();
+        if constexpr (!WHOLE) {
+          if (oh + lane < O) {
+            float* yp = static_cast<float*>(epi.y) + tj * epi.ldy + oh + lane;
+            const int rows = (int)(T - tj < 32 ? T - tj : 32);
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r, yp += epi.ldy) {
+              const float e = *reinterpret_cast<const float*>(mine + r * 256 + 16 * ((lane >> 2) ^ (r & 15)) + 4 * (lane & 3));
+              *yp = epi.accumulate ? *yp + e : e;
+            }
+          }
+          __builtin_amdgcn_wave_barrier();
+          continue;
+        }
         f32x4 d[8];
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
@@ -662,7 +748,7 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
           const int64_t t = tj + 4 * p + (lane >> 4), o = oh + 4 * (lane & 15);
           if (t >= T || o >= O) continue;
           float* yp = static_cast<float*>(epi.y) + t * epi.ldy + o;
-          if (rows16 && o + 4 <= O) {
+          if (o + 4 <= O) {
             if (epi.accumulate) d[p] += *reinterpret_cast<const f32x4*>(yp);
             *reinterpret_cast<f32x4*>(yp) = d[p];
           } else {
@@ -855,7 +941,10 @@ __global__ __launch_bounds__(256) void k_i8_big(
   bar();
   mma_done(acc);
   const int ow = GLU ? wmi * 64 : wmi * 128;
-  i8_finish_big<GLU>(acc, epi, T, O, o0 + ow, t0 + wni * 128, lane, s0 + wave * 8192, sw, ow);
+  if (epi.bf16_out ? epi.ldy % 8 == 0 : epi.ldy % 4 == 0)
+    i8_finish_big<GLU, true>(acc, epi, T, O, o0 + ow, t0 + wni * 128, lane, s0 + wave * 8192, sw, ow);
+  else
+    i8_finish_big<GLU, false>(acc, epi, T, O, o0 + ow, t0 + wni * 128, lane, s0 + wave * 8192, sw, ow);
 }
 
 template <int BM, int BN, int WM, int WN, bool SP, bool GLU, int NST>

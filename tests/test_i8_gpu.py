@@ -246,6 +246,8 @@ def test_product_larger_shapes(sparse):
                     (700, 1024, 1536), (1100, 2100, 640)]:
         check_product(rng, t, o, k, sparse)
         check_product(rng, t, o, k, sparse, bf16=True, ldy=up(o, 8))
+        check_product(rng, t, o, k, sparse, bf16=True, shift=1, ldy=o + 1 - o % 2)
+        check_product(rng, t, o, k, sparse, accumulate=1, ldy=o + 1 - o % 2)
 
 
 SPLIT_SHAPES = [(1, 65, 32768), (8, 501, 32768), (16, 512, 14336), (40, 258, 14336), (61, 1030, 8192), (130, 300, 9000),
@@ -371,6 +373,7 @@ def test_glu(sparse, act):
         for big in (1.0, 40.0):
             check_glu(rng, t, o, k, sparse, act, routes=tuple(ROUTES), big=big, ldy=o + t % 2)
         check_glu(rng, t, o, k, sparse, act, routes=tuple(ROUTES), bf16=True, ldy=up(o, 8))
+        check_glu(rng, t, o, k, sparse, act, routes=tuple(ROUTES), bf16=True, ldy=o + 1 - o % 2)
     for t, o, k in [(1, 2048, 4096), (8, 14336, 256), (600, 1030, 1024), (1100, 1100, 640)]:
         check_glu(rng, t, o, k, sparse, act)
         check_glu(rng, t, o, k, sparse, act, bf16=True)
