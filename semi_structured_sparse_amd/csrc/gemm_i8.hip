@@ -217,7 +217,7 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
             *reinterpret_cast<uint2*>(mine + fr * 128 + 16 * ((2 * i + (fq >> 1)) ^ (fr & 7)) + 8 * (fq & 1)) =
                 make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
           }
-          __builtin_amdgcn_wave_barrier();
+          wave_lds_fence();
           if (!whole) {
             if (oh + lane < O) {
               uint16_t* yp = static_cast<uint16_t*>(epi.y) + (tb_w + 16 * j) * epi.ldy + oh + lane;
@@ -226,7 +226,7 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
               for (int r = 0; r < rows; ++r, yp += epi.ldy)
                 *yp = *reinterpret_cast<const uint16_t*>(mine + r * 128 + 16 * ((lane >> 3) ^ (r & 7)) + 2 * (lane & 7));
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_lds_fence();
             continue;
           }
           uint4 d[2];
@@ -235,7 +235,7 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
             const int row = 8 * p + (lane >> 3);
             d[p] = *reinterpret_cast<const uint4*>(mine + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
           }
-          __builtin_amdgcn_wave_barrier();
+          wave_lds_fence();
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const int64_t t = tb_w + 16 * j + 8 * p + (lane >> 3), o = oh + 8 * (lane & 7);
@@ -267,7 +267,7 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<f32x4*>(mine + fr * 256 + 16 * ((4 * i + fq) ^ fr)) = values(sc[i], 4 * h + i, j);
-          __builtin_amdgcn_wave_barrier();
+          wave_lds_fence();
           if (!whole) {
             if (oh + lane < O) {
               float* yp = static_cast<float*>(epi.y) + (tb_w + 16 * j) * epi.ldy + oh + lane;
@@ -278,7 +278,7 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
                 *yp = epi.accumulate ? *yp + e : e;
               }
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_lds_fence();
             continue;
           }
           f32x4 d[4];
@@ -287,7 +287,7 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
             const int row = 4 * p + (lane >> 4);
             d[p] = *reinterpret_cast<const f32x4*>(mine + row * 256 + 16 * ((lane & 15) ^ (row & 15)));
           }
-          __builtin_amdgcn_wave_barrier();
+          wave_lds_fence();
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const int64_t t = tb_w + 16 * j + 4 * p + (lane >> 4), o = oh + 4 * (lane & 15);
@@ -352,12 +352,12 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
     for (int j = 0; j < FJ; ++j) {
 #pragma unroll
       for (int i = 0; i < NO; ++i) *reinterpret_cast<f32x4*>(mine + piece(fr, 4 * i + fq)) = values(scales(i), i, j);
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_fence();
       float e[W / 4];
 #pragma unroll
       for (int p = 0; p < W / 4; ++p)
         e[p] = *reinterpret_cast<const float*>(mine + piece(64 / W * p + lane / W, lane % W / 4) + 4 * (lane & 3));
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_fence();
 #pragma unroll
       for (int p = 0; p < W / 4; ++p) {
         const int64_t t = tb_w + 16 * j + 64 / W * p + lane / W;
@@ -679,7 +679,7 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
             *reinterpret_cast<uint2*>(mine + c * 128 + 16 * (p ^ ((c >> 1) & 7)) + 8 * h) =
                 make_uint2(bf16x2(v[b][g][0], v[b][g][1]), bf16x2(v[b][g][2], v[b][g][3]));
           }
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_fence();
         if constexpr (!WHOLE) {
           if (oh + lane < O) {
             uint16_t* yp = static_cast<uint16_t*>(epi.y) + tj * epi.ldy + oh + lane;
@@ -688,7 +688,7 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
             for (int r = 0; r < rows; ++r, yp += epi.ldy)
               *yp = *reinterpret_cast<const uint16_t*>(mine + r * 128 + 16 * ((lane >> 3) ^ ((r >> 1) & 7)) + 2 * (lane & 7));
           }
-          __builtin_amdgcn_wave_barrier();
+          wave_lds_fence();
           continue;
         }
         uint4 d[4];
@@ -697,7 +697,7 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
           const int row = 8 * p + (lane >> 3);
           d[p] = *reinterpret_cast<const uint4*>(mine + row * 128 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_fence();
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const int64_t t = tj + 8 * p + (lane >> 3), o = oh + 8 * (lane & 7);
@@ -722,7 +722,7 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
             *reinterpret_cast<f32x4*>(mine + c * 256 + 16 * (p ^ (c & 15))) =
                 f32x4{v[b][g][0], v[b][g][1], v[b][g][2], v[b][g][3]};
           }
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_fence();
         if constexpr (!WHOLE) {
           if (oh + lane < O) {
             float* yp = static_cast<float*>(epi.y) + tj * epi.ldy + oh + lane;
@@ -733,7 +733,7 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
               *yp = epi.accumulate ? *yp + e : e;
             }
           }
-          __builtin_amdgcn_wave_barrier();
+          wave_lds_fence();
           continue;
         }
         f32x4 d[8];
@@ -742,7 +742,7 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
           const int row = 4 * p + (lane >> 4);
           d[p] = *reinterpret_cast<const f32x4*>(mine + row * 256 + 16 * ((lane & 15) ^ (row & 15)));
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_fence();
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
           const int64_t t = tj + 4 * p + (lane >> 4), o = oh + 4 * (lane & 15);

@@ -10,6 +10,14 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 // Sixteen readable zero bytes: where loads past the end of a row go.
 static __device__ const uint4 kZero16 = {0u, 0u, 0u, 0u};
 
+// Between a wave's writes to LDS and its reads of them as another type (either way round): LDS
+// serves one wave in order, and the compiler moves or merges no access across.
+__device__ __forceinline__ void wave_lds_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Gate of a GLU in fp32.  silu: g / (1 + e^-g).  gelu: (1 + tanh z) / 2 = 1 / (1 + e^-2z), the
 // same function without the cancellation of 1 + tanh z for negative z (2 sqrt(2/pi) =
 // 1.5957691).  Where the exponential overflows the gate is its limit, -0 (g = -inf enters the

@@ -20,8 +20,7 @@
 // The kernel moves 2 + 1 (lifted 2 + 2(N-1)/N) bytes per value and is bound by memory: 8191 x
 // 4096 lifted for 6:8 (118 MB) 18.2 us, 6.5 TB/s (part of it from the last-level cache); with a
 // selection also by its network, 2048 x 14336 at 8:16 (88 MB) 21.8 us, 4.0 TB/s; one row 2.5 us.
-#include "i8_launch.h"
-#include "nm_device.h"
+#include "i8_device.h"
 
 namespace {
 
@@ -192,7 +191,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_quant_i8(
     if (tid < (kl16 - kl) / 4) reinterpret_cast<uint32_t*>(qr + kl)[tid] = 0u;
   }
   if constexpr (LIFT == 1) {
-    if constexpr (WAVE) __builtin_amdgcn_wave_barrier();
+    if constexpr (WAVE) wave_lds_fence();
     else __syncthreads();
     const uint32_t wpg = (uint32_t)(ns - 1);
     const int dwords = k / (2 * ns) * (ns - 1);

@@ -267,8 +267,8 @@ def test_split_reductions(sparse):
 
 
 @pytest.mark.parametrize("sparse", [False, True])
-def test_ring_tiles_give_the_same_bits_every_time(sparse):
-    """Each of the smaller tiles, many workgroups a CU and long reductions, 60 calls."""
+def test_tiles_give_the_same_bits_every_time(sparse):
+    """Smaller and 256 x 256 tiles, several workgroups a CU and long reductions, call after call."""
     rng = np.random.default_rng(46 + sparse)
     for t, o, k in [(700, 1024, 4096), (500, 1536, 4096), (700, 2048, 2048), (1024, 3000, 1024)]:
         x = torch.from_numpy(random_codes(rng, t, k, k, True)).cuda()
@@ -276,11 +276,11 @@ def test_ring_tiles_give_the_same_bits_every_time(sparse):
         ones_t, ones_o = torch.ones(t, device="cuda"), torch.ones(o, device="cuda")
         want, y = (torch.empty(t, o + 1, device="cuda") for _ in range(2))
         S.nm_spmm_i8(x, ones_t, wd, ones_o, want, meta, k=k, route=ROUTES["stream"])
-        for _ in range(60):
+        for i in range(90):
             y.fill_(float("nan"))
-            S.nm_spmm_i8(x, ones_t, wd, ones_o, y, meta, k=k, route=ROUTES["split"])
+            S.nm_spmm_i8(x, ones_t, wd, ones_o, y, meta, k=k, route=ROUTES["split" if i % 3 else "tile"])
             sync()
-            assert torch.equal(y[:, :o], want[:, :o]), (t, o, k)
+            assert torch.equal(y[:, :o], want[:, :o]), (t, o, k, i)
 
 
 def test_longest_reduction_stays_inside_32_bits():
