@@ -529,6 +529,18 @@ def _mat(t, dev, size=0):
     return t.data_ptr(), st[0]
 
 
+def _holds(t, rows, cols, whole, ld):
+    """Refuses a matrix with fewer rows or columns (counted up to a whole piece of `whole` elements,
+    which a row's padding completes), or whose last row's pieces end past its storage."""
+    sh = t.shape
+    if sh[0] < rows or sh[1] + -sh[1] % whole < cols:
+        raise ValueError(f"a matrix of {rows} rows of {cols} elements is needed")
+    if rows > 0 and cols > 0:
+        end = t.storage_offset() + (rows - 1) * ld + cols + -cols % whole
+        if end * t.element_size() > t.untyped_storage().nbytes():
+            raise ValueError(f"the storage ends inside the last of {rows} rows of {cols} elements, {ld} apart")
+
+
 def _factors(t, n, dev):
     """_vec of at least n contiguous fp32 values."""
     if t is None or type(t) is int:
@@ -573,8 +585,13 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
         k = x.shape[1]
     if type(x) is not int and x is not None and x.dtype is _half:
         raise ValueError("x of bf16 values is needed")
-    if q is not None and type(q) is not int and q.shape[0] < rows:
-        raise ValueError(f"q of {rows} rows is needed")
+    if q is not None and type(q) is not int:
+        kq = k // (2 * ns) * 4 * (ns - 1) if ns > 2 else k
+        width = q.shape[1]
+        if width < kq:
+            raise ValueError(f"q of rows of {kq} codes is needed")
+        if q.shape[0] < rows or width & 15 or ldq is not None:
+            _holds(q, rows, kq, 16, lq if ldq is None else ldq)
     st = lib().nm_quant_i8(xp, rows, k, lx if ldx is None else ldx, n, m, ns, qp, lq if ldq is None else ldq,
                            _factors(scale, rows, dev), _stream(stream))
     if check and st:

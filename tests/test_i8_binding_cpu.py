@@ -1,0 +1,74 @@
+"""What the int8 entry points of the binding accept of their tensors, without a GPU: the library is
+replaced by a recorder and the tensors live on the CPU (the binding takes -1, their device, for
+the current one).  A call whose memory the tensors do not hold must be refused before the
+library is reached; the calls that the layouts allow must reach it with the right arguments."""
+import pytest
+
+import semi_structured_sparse_amd as S
+
+torch = pytest.importorskip("torch")
+
+
+class Recorder:
+    """Stands for the loaded library: every entry point notes its arguments and succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    rec = Recorder()
+    monkeypatch.setattr(S, "lib", lambda: rec)
+    monkeypatch.setattr(S, "_current_device", lambda: -1)
+    monkeypatch.setattr(S, "_current_raw_stream", lambda: 0)
+    monkeypatch.setattr(S, "_half", torch.float16)
+    return rec.calls
+
+
+def refused(calls, f, *args, **kw):
+    before = len(calls)
+    with pytest.raises(ValueError):
+        f(*args, **kw)
+    assert len(calls) == before, "the library was reached"
+
+
+def taken(calls, f, *args, **kw):
+    """Arguments that the library received."""
+    before = len(calls)
+    assert f(*args, **kw) == 0
+    assert len(calls) == before + 1
+    return calls[-1][1]
+
+
+def bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def i8(*shape):
+    return torch.zeros(*shape, dtype=torch.int8)
+
+
+# ------------------------------------------------------------------------------- nm_quant_i8 ---
+
+def test_quant_refuses_codes_narrower_than_their_rows(calls):
+    x, s = bf16(4, 64), torch.zeros(4)
+    refused(calls, S.nm_quant_i8, x, i8(4, 256)[:, 192:256], s, ns=4)      # 96 codes a row
+    refused(calls, S.nm_quant_i8, x, i8(4, 256)[:, :48], s)
+    refused(calls, S.nm_quant_i8, x, i8(4, 256)[:, :64], s, ns=4)
+    refused(calls, S.nm_quant_i8, x, i8(4, 64), s, ldq=80)                  # the last row ends past the tensor
+    flat = i8(4 * 64 - 14)                                                 # rows of 50 codes: the last one's pad is cut off
+    refused(calls, S.nm_quant_i8, x, flat.as_strided((4, 50), (64, 1)), s, k=50)
+    refused(calls, S.nm_quant_i8, x, i8(3, 64), s)
+    a = taken(calls, S.nm_quant_i8, x, i8(4, 256)[:, 128:224], s, ns=4)
+    assert a[8] == 256
+    q = i8(4 * 64)
+    a = taken(calls, S.nm_quant_i8, x, q.as_strided((4, 50), (64, 1)), s, k=50)   # its pad is there
+    assert a[7] == q.data_ptr() and a[8] == 64
+    a = taken(calls, S.nm_quant_i8, x, i8(8, 64), s, ldq=128)                   # every second row
+    assert a[8] == 128
+    taken(calls, S.nm_quant_i8, x, 1 << 20, s, ldq=64)                      # a raw pointer is the caller's
+    taken(calls, S.nm_quant_i8, x[:0], i8(0, 64), s)
