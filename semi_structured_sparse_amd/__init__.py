@@ -579,21 +579,29 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
     dev = _device() if stream is None else _device_of(x, q, scale)
     xp, lx = _mat(x, dev, 2)
     qp, lq = _mat(q, dev, 1)
-    if rows is None:
-        rows = x.shape[0]
-    if k is None:
-        k = x.shape[1]
-    if type(x) is not int and x is not None and x.dtype is _half:
-        raise ValueError("x of bf16 values is needed")
-    if q is not None and type(q) is not int:
+    if ldq is not None:
+        lq = ldq
+    if xp is not x:                      # a tensor
+        have, width = x.shape
+        if rows is None:
+            rows = have
+        if k is None:
+            k = width
+        if x.dtype is _half:
+            raise ValueError("x of bf16 values is needed")
+        if width < k:
+            raise ValueError(f"x of rows of {k} values is needed")
+        if have < rows or width & 7 or ldx is not None:
+            _holds(x, rows, k, 8, lx if ldx is None else ldx)
+    if qp is not q:
+        have, width = q.shape
         kq = k // (2 * ns) * 4 * (ns - 1) if ns > 2 else k
-        width = q.shape[1]
         if width < kq:
             raise ValueError(f"q of rows of {kq} codes is needed")
-        if q.shape[0] < rows or width & 15 or ldq is not None:
-            _holds(q, rows, kq, 16, lq if ldq is None else ldq)
-    st = lib().nm_quant_i8(xp, rows, k, lx if ldx is None else ldx, n, m, ns, qp, lq if ldq is None else ldq,
-                           _factors(scale, rows, dev), _stream(stream))
+        if have < rows or width & 15 or ldq is not None:
+            _holds(q, rows, kq, 16, lq)
+    st = lib().nm_quant_i8(xp, rows, k, lx if ldx is None else ldx, n, m, ns, qp, lq, _factors(scale, rows, dev),
+                           _stream(stream))
     if check and st:
         _check(st, "nm_quant_i8")
     return st

@@ -72,3 +72,21 @@ def test_quant_refuses_codes_narrower_than_their_rows(calls):
     assert a[8] == 128
     taken(calls, S.nm_quant_i8, x, 1 << 20, s, ldq=64)                      # a raw pointer is the caller's
     taken(calls, S.nm_quant_i8, x[:0], i8(0, 64), s)
+
+
+def test_quant_refuses_values_that_x_does_not_hold(calls):
+    q, s = i8(64, 256), torch.zeros(64)
+    refused(calls, S.nm_quant_i8, bf16(4, 64), q, s, rows=64)
+    refused(calls, S.nm_quant_i8, bf16(4, 64), q, s, k=72)
+    refused(calls, S.nm_quant_i8, bf16(4, 256)[:, :64], q, s, k=72)
+    refused(calls, S.nm_quant_i8, bf16(4, 64), q, s, ldx=72)                # the last row ends past the tensor
+    flat = bf16(3 * 56 + 50)                                               # pieces of 8: the last row needs 56 values
+    refused(calls, S.nm_quant_i8, flat.as_strided((4, 50), (56, 1)), q, s)
+    flat = bf16(4 * 56)
+    a = taken(calls, S.nm_quant_i8, flat.as_strided((4, 50), (56, 1)), q, s)
+    assert a[:4] == (flat.data_ptr(), 4, 50, 56)
+    a = taken(calls, S.nm_quant_i8, bf16(4, 56), q, s, k=50)                # padded rows
+    assert a[1:4] == (4, 50, 56)
+    a = taken(calls, S.nm_quant_i8, bf16(8, 64), q, s, rows=4, ldx=128)     # every second row
+    assert a[1:4] == (4, 64, 128)
+    taken(calls, S.nm_quant_i8, 1 << 20, q, s, rows=64, k=64, ldx=64)       # a raw pointer is the caller's
