@@ -561,13 +561,18 @@ def _i8_out(y, t, o, dev):
     return p, ld, NM_Y_F32 if size == 4 else NM_Y_BF16
 
 
-def _meta(t, o, k, dev):
-    """Pointer of blocked positions (nm_meta_block) of at least o rows over k."""
+def _packed(t, size, dev):
+    """Pointer of at least `size` contiguous bytes of positions."""
     if t is None or type(t) is int:
         return t
-    if t.get_device() != dev or t.numel() * t.element_size() < (k + 127) // 128 * o * 16 or not t.is_contiguous():
-        _refuse(t, dev, "contiguous blocked positions of all rows are needed")
+    if t.get_device() != dev or t.numel() * t.element_size() < size or not t.is_contiguous():
+        _refuse(t, dev, f"{size} contiguous bytes of positions are needed")
     return t.data_ptr()
+
+
+def _meta(t, o, k, dev):
+    """Pointer of blocked positions (nm_meta_block) of at least o rows over k."""
+    return t if t is None else _packed(t, (k + 127) // 128 * o * 16, dev)
 
 
 def _bytes(t):
@@ -608,8 +613,9 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
 
 
 def nm_meta_block(meta, o, kc, out, stream=None, *, check=True):
+    """2-bit positions in rows -> step blocks (include/nm.h); both tensors contiguous."""
     dev = _device() if stream is None else _device_of(meta, out)
-    st = lib().nm_meta_block(_vec(meta, dev), o, kc, _vec(out, dev), _stream(stream))
+    st = lib().nm_meta_block(_packed(meta, o * ((kc + 7) // 8), dev), o, kc, _meta(out, o, kc, dev), _stream(stream))
     if check:
         _check(st, "nm_meta_block")
     return st

@@ -90,3 +90,23 @@ def test_quant_refuses_values_that_x_does_not_hold(calls):
     a = taken(calls, S.nm_quant_i8, bf16(8, 64), q, s, rows=4, ldx=128)     # every second row
     assert a[1:4] == (4, 64, 128)
     taken(calls, S.nm_quant_i8, 1 << 20, q, s, rows=64, k=64, ldx=64)       # a raw pointer is the caller's
+
+
+# ----------------------------------------------------------------------------- nm_meta_block ---
+
+def u8(*shape):
+    return torch.zeros(*shape, dtype=torch.uint8)
+
+
+def test_meta_block_refuses_positions_that_do_not_fit(calls):
+    meta, out = u8(5, 17), u8(2 * 5 * 16)                                   # kc = 132: two step blocks
+    refused(calls, S.nm_meta_block, meta, 5, 132, out[:-16])
+    refused(calls, S.nm_meta_block, meta, 5, 132, u8(2, 5, 17)[:, :, :16])  # blocks with gaps
+    refused(calls, S.nm_meta_block, meta[:4], 5, 132, out)
+    refused(calls, S.nm_meta_block, u8(5, 16), 5, 132, out)
+    refused(calls, S.nm_meta_block, u8(5, 32)[:, :17], 5, 132, out)         # rows of meta lie 17 bytes apart
+    a = taken(calls, S.nm_meta_block, meta, 5, 132, out)
+    assert a[:4] == (meta.data_ptr(), 5, 132, out.data_ptr())
+    taken(calls, S.nm_meta_block, torch.zeros(5, 9, dtype=torch.int16), 5, 132, torch.zeros(40, dtype=torch.int32))
+    taken(calls, S.nm_meta_block, 1 << 20, 5, 132, 1 << 24)
+    taken(calls, S.nm_meta_block, u8(0, 17), 0, 132, u8(0))
