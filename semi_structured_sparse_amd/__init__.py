@@ -541,6 +541,25 @@ def _holds(t, rows, cols, whole, ld):
             raise ValueError(f"the storage ends inside the last of {rows} rows of {cols} elements, {ld} apart")
 
 
+def _shape(t):
+    return None if t is None or type(t) is int else t.shape
+
+
+def _codes(m, sh, dev, rows, cols, ld):
+    """(pointer, leading dimension) of int8 codes of shape sh that are read: `rows` rows of `cols`, in
+    pieces of 16; ld: None, or a leading dimension in place of the tensor's."""
+    if sh is None:
+        return m, ld or 0
+    st = m.stride()
+    if len(st) != 2 or st[1] != 1 or m.get_device() != dev or m.element_size() != 1:
+        _refuse(m, dev, "a matrix with contiguous rows of 1-byte elements is needed")
+    if ld is None:
+        ld = st[0]
+    if sh[0] < rows or sh[1] < cols + -cols % 16 or ld != st[0]:
+        _holds(m, rows, cols, 16, ld)
+    return m.data_ptr(), ld
+
+
 def _factors(t, n, dev):
     """_vec of at least n contiguous fp32 values."""
     if t is None or type(t) is int:
@@ -636,17 +655,18 @@ def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift
     nm_meta_block): 2:4 weights.  k: the reduction length where it is not x's width.
     taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
     dev = _device() if stream is None else _device_of(x, w, y)
-    xp, lx = _mat(x, dev, 1)
-    wp, lw = _mat(w, dev, 1)
+    sx, sw = _shape(x), _shape(w)
     if t is None:
-        t = x.shape[0]
+        t = sx[0]
     if o is None:
-        o = w.shape[0]
+        o = sw[0]
     if k is None:
-        k = x.shape[1]
+        k = sx[1]
+    xp, lx = _codes(x, sx, dev, t, k, ldx)
+    wp, lw = _codes(w, sw, dev, o, k if w_meta is None else k // 2, ldw)
     yp, ly, yd = _i8_out(y, t, o, dev)
-    st = lib().nm_spmm_i8(xp, t, k, lx if ldx is None else ldx, _factors(x_scale, t, dev), wp, o,
-                          lw if ldw is None else ldw, _factors(w_scale, o, dev), _meta(w_meta, o, k, dev),
+    st = lib().nm_spmm_i8(xp, t, k, lx, _factors(x_scale, t, dev), wp, o,
+                          lw, _factors(w_scale, o, dev), _meta(w_meta, o, k, dev),
                           _factors(row_shift, t, dev), _factors(col_shift, o, dev), yp,
                           ly if ldy is None else ldy, yd if y_dtype is None else y_dtype, accumulate,
                           _vec(workspace, dev), _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
@@ -662,25 +682,25 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
     """y = act(x . w_gate^T) * (x . w_up^T), each with its scales, in 8-bit integers.
     taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
     dev = _device() if stream is None else _device_of(x, w_gate, y)
-    xp, lx = _mat(x, dev, 1)
-    gp, lg = _mat(w_gate, dev, 1)
-    up, lu = _mat(w_up, dev, 1)
-    if ldw is None:
-        if lg != lu:
-            raise ValueError("w_gate and w_up need the same leading dimension")
-        ldw = lg
+    sx, sg, su = _shape(x), _shape(w_gate), _shape(w_up)
     if t is None:
-        t = x.shape[0]
+        t = sx[0]
     if inter is None:
-        inter = w_gate.shape[0]
-        if type(w_up) is not int and w_up.shape[0] != inter:
+        inter = sg[0]
+        if su is not None and su[0] != inter:
             raise ValueError("w_gate and w_up need the same rows")
     if k is None:
-        k = x.shape[1]
+        k = sx[1]
+    xp, lx = _codes(x, sx, dev, t, k, ldx)
+    kw = k if gate_meta is None else k // 2
+    gp, lg = _codes(w_gate, sg, dev, inter, kw, ldw)
+    up, lu = _codes(w_up, su, dev, inter, kw, ldw)
+    if lg != lu:
+        raise ValueError("w_gate and w_up need the same leading dimension")
     yp, ly, yd = _i8_out(y, t, inter, dev)
-    st = lib().nm_glu_i8(xp, t, k, lx if ldx is None else ldx, _factors(x_scale, t, dev), gp,
+    st = lib().nm_glu_i8(xp, t, k, lx, _factors(x_scale, t, dev), gp,
                          _factors(gate_scale, inter, dev), _meta(gate_meta, inter, k, dev), up,
-                         _factors(up_scale, inter, dev), _meta(up_meta, inter, k, dev), inter, ldw, act, yp,
+                         _factors(up_scale, inter, dev), _meta(up_meta, inter, k, dev), inter, lg, act, yp,
                          ly if ldy is None else ldy, yd if y_dtype is None else y_dtype, _vec(workspace, dev),
                          _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
                          ctypes.addressof(taken) if taken is not None else None, _stream(stream))

@@ -110,3 +110,50 @@ def test_meta_block_refuses_positions_that_do_not_fit(calls):
     taken(calls, S.nm_meta_block, torch.zeros(5, 9, dtype=torch.int16), 5, 132, torch.zeros(40, dtype=torch.int32))
     taken(calls, S.nm_meta_block, 1 << 20, 5, 132, 1 << 24)
     taken(calls, S.nm_meta_block, u8(0, 17), 0, 132, u8(0))
+
+
+# -------------------------------------------------------------------------------- products ---
+
+def product(x, w, y, w_meta=None, **kw):
+    return S.nm_spmm_i8(x, torch.ones(64), w, torch.ones(64), y, w_meta, **kw)
+
+
+def gated(x, w, y, w_meta=None, up=None, **kw):
+    if "o" in kw:
+        kw["inter"] = kw.pop("o")
+    return S.nm_glu_i8(x, torch.ones(64), w, torch.ones(64), w if up is None else up, torch.ones(64), y,
+                       gate_meta=w_meta, up_meta=w_meta, **kw)
+
+
+@pytest.mark.parametrize("call", [product, gated])
+def test_products_refuse_operands_that_are_not_there(calls, call):
+    y = torch.zeros(64, 64)
+    x, w, meta = i8(4, 64), i8(8, 64), u8(8 * 16)
+    refused(calls, call, x, w, y, t=64)
+    refused(calls, call, x, w, y, o=64)
+    refused(calls, call, x, i8(8, 128), y, k=128)
+    refused(calls, call, i8(4, 128), w, y)                                  # x's width is the reduction
+    refused(calls, call, x, i8(8, 32), y)                                   # dense weights of half the length
+    refused(calls, call, x, i8(8, 16), y, meta)                             # 2:4: 32 values a row
+    refused(calls, call, x, w, y, ldx=80)                                   # last rows past the tensors' ends
+    refused(calls, call, x, w, y, ldw=80)
+    refused(calls, call, i8(4 * 64 - 14).as_strided((4, 50), (64, 1)), w, y)
+    refused(calls, call, x, i8(8 * 64 - 14).as_strided((8, 50), (64, 1)), y, k=50)
+    flat = i8(4 * 64)
+    a = taken(calls, call, flat.as_strided((4, 50), (64, 1)), w, y)         # its pad is there
+    assert a[:4] == (flat.data_ptr(), 4, 50, 64)
+    a = taken(calls, call, i8(4, 112), i8(8, 112)[:, :100], y)              # W's pad counts: X is zero there
+    assert a[1:4] == (4, 112, 112)
+    taken(calls, call, x, w, y, meta)                                       # wider than its 32 values
+    taken(calls, call, x, i8(8, 32), y, meta)
+    a = taken(calls, call, i8(8, 64), i8(16, 64), y, t=4, o=8, ldx=128, ldw=128)   # every second row
+    assert a[1:4] == (4, 64, 128)
+    taken(calls, call, 1 << 20, w, y, t=64, k=64, ldx=64)                   # a raw pointer is the caller's
+
+
+def test_gated_products_check_both_weights(calls):
+    y, x, w = torch.zeros(64, 64), i8(4, 64), i8(8, 64)
+    refused(calls, gated, x, w, y, up=i8(8, 64)[:7], o=8)
+    refused(calls, gated, x, w, y, up=i8(8 * 64 - 1).as_strided((8, 63), (64, 1)))
+    refused(calls, gated, x, w, y, up=i8(8, 32), ldw=64)
+    taken(calls, gated, x, w, y, up=i8(9, 64), o=8)
