@@ -519,13 +519,13 @@ def _vec(t, dev):
     return t.data_ptr()
 
 
-def _mat(t, dev, size=0):
-    """(pointer, leading dimension) of a matrix with contiguous rows (of `size`-byte elements)."""
+def _mat(t, dev, size):
+    """(pointer, leading dimension) of a matrix with contiguous rows of `size`-byte elements."""
     if t is None or type(t) is int:
         return t, 0
     st = t.stride()
-    if len(st) != 2 or st[1] != 1 or t.get_device() != dev or (size and t.element_size() != size):
-        _refuse(t, dev, f"a matrix with contiguous rows{f' of {size}-byte elements' if size else ''} is needed")
+    if len(st) != 2 or st[1] != 1 or t.get_device() != dev or t.element_size() != size:
+        _refuse(t, dev, f"a matrix with contiguous rows of {size}-byte elements is needed")
     return t.data_ptr(), st[0]
 
 
@@ -569,15 +569,20 @@ def _factors(t, n, dev):
     return t.data_ptr()
 
 
-def _i8_out(y, t, o, dev):
-    """(pointer, leading dimension, NM_Y_*) of an output of at least t rows of o (raw pointers: fp32)."""
-    p, ld = _mat(y, dev)
+def _i8_out(y, t, o, dev, ld, dtype):
+    """(pointer, leading dimension, NM_Y_*) of an output of at least t rows of o (raw pointers: fp32
+    unless dtype says otherwise); ld: None, or a leading dimension in place of the tensor's."""
     if y is None or type(y) is int:
-        return p, ld, NM_Y_F32
-    size, shape = y.element_size(), y.shape
-    if (size != 4 and size != 2) or shape[0] < t or shape[1] < o or y.dtype is _half:
-        raise ValueError(f"y of {t} rows of {o} fp32 or bf16 values is needed")
-    return p, ld, NM_Y_F32 if size == 4 else NM_Y_BF16
+        return y, ld or 0, NM_Y_F32 if dtype is None else dtype
+    st, sh, size = y.stride(), y.shape, y.element_size()
+    kind = NM_Y_F32 if size == 4 else NM_Y_BF16
+    if (len(st) != 2 or st[1] != 1 or y.get_device() != dev or (size != 4 and size != 2) or y.dtype is _half
+            or sh[0] < t or sh[1] < o or (dtype is not None and dtype != kind)):
+        _refuse(y, dev, f"y of {t} contiguous rows of {o} fp32 or bf16 values is needed")
+    if ld is None:
+        return y.data_ptr(), st[0], kind
+    _holds(y, t, o, 1, ld)
+    return y.data_ptr(), ld, kind
 
 
 def _packed(t, size, dev):
@@ -664,11 +669,10 @@ def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift
         k = sx[1]
     xp, lx = _codes(x, sx, dev, t, k, ldx)
     wp, lw = _codes(w, sw, dev, o, k if w_meta is None else k // 2, ldw)
-    yp, ly, yd = _i8_out(y, t, o, dev)
+    yp, ly, yd = _i8_out(y, t, o, dev, ldy, y_dtype)
     st = lib().nm_spmm_i8(xp, t, k, lx, _factors(x_scale, t, dev), wp, o,
                           lw, _factors(w_scale, o, dev), _meta(w_meta, o, k, dev),
-                          _factors(row_shift, t, dev), _factors(col_shift, o, dev), yp,
-                          ly if ldy is None else ldy, yd if y_dtype is None else y_dtype, accumulate,
+                          _factors(row_shift, t, dev), _factors(col_shift, o, dev), yp, ly, yd, accumulate,
                           _vec(workspace, dev), _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
                           ctypes.addressof(taken) if taken is not None else None, _stream(stream))
     if check and st:
@@ -697,12 +701,11 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
     up, lu = _codes(w_up, su, dev, inter, kw, ldw)
     if lg != lu:
         raise ValueError("w_gate and w_up need the same leading dimension")
-    yp, ly, yd = _i8_out(y, t, inter, dev)
+    yp, ly, yd = _i8_out(y, t, inter, dev, ldy, y_dtype)
     st = lib().nm_glu_i8(xp, t, k, lx, _factors(x_scale, t, dev), gp,
                          _factors(gate_scale, inter, dev), _meta(gate_meta, inter, k, dev), up,
-                         _factors(up_scale, inter, dev), _meta(up_meta, inter, k, dev), inter, lg, act, yp,
-                         ly if ldy is None else ldy, yd if y_dtype is None else y_dtype, _vec(workspace, dev),
-                         _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
+                         _factors(up_scale, inter, dev), _meta(up_meta, inter, k, dev), inter, lg, act, yp, ly, yd,
+                         _vec(workspace, dev), _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
                          ctypes.addressof(taken) if taken is not None else None, _stream(stream))
     if check and st:
         _check(st, "nm_glu_i8")

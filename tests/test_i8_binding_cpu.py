@@ -157,3 +157,23 @@ def test_gated_products_check_both_weights(calls):
     refused(calls, gated, x, w, y, up=i8(8 * 64 - 1).as_strided((8, 63), (64, 1)))
     refused(calls, gated, x, w, y, up=i8(8, 32), ldw=64)
     taken(calls, gated, x, w, y, up=i8(9, 64), o=8)
+
+
+@pytest.mark.parametrize("call", [product, gated])
+def test_products_refuse_outputs_written_past_their_end(calls, call):
+    x, w = i8(4, 64), i8(8, 64)
+    y = torch.zeros(4, 8)
+    refused(calls, call, x, w, y, ldy=9)
+    refused(calls, call, x, w, y.bfloat16(), y_dtype=S.NM_Y_F32)             # twice its bytes
+    refused(calls, call, x, w, y, y_dtype=S.NM_Y_BF16)
+    refused(calls, call, x, w, torch.zeros(16, 8)[:4], t=8)
+    refused(calls, call, x, w, torch.zeros(4, 7), y_dtype=S.NM_Y_F32)
+    for dt in (torch.float32, torch.bfloat16, torch.int16):
+        out = torch.zeros(8, 8, dtype=dt)
+        a = taken(calls, call, x, w, out, ldy=16)                            # every second row
+        at = a.index(out.data_ptr())
+        assert a[at + 1:at + 3] == (16, S.NM_Y_F32 if dt is torch.float32 else S.NM_Y_BF16)
+        taken(calls, call, x, w, out[:4], y_dtype=S.NM_Y_F32 if dt is torch.float32 else S.NM_Y_BF16)
+    a = taken(calls, call, x, w, 1 << 20, o=8, ldy=8, y_dtype=S.NM_Y_BF16)   # a raw pointer is the caller's
+    at = a.index(1 << 20)
+    assert a[at + 1:at + 3] == (8, S.NM_Y_BF16)
