@@ -510,15 +510,6 @@ def _refuse(t, dev, what):
     raise ValueError(what)
 
 
-def _vec(t, dev):
-    """Pointer of a tensor on device dev (None -> NULL, integers are raw pointers)."""
-    if t is None or type(t) is int:
-        return t
-    if t.get_device() != dev:
-        _refuse(t, dev, "")
-    return t.data_ptr()
-
-
 def _mat(t, dev, size):
     """(pointer, leading dimension) of a matrix with contiguous rows of `size`-byte elements."""
     if t is None or type(t) is int:
@@ -561,7 +552,7 @@ def _codes(m, sh, dev, rows, cols, ld):
 
 
 def _factors(t, n, dev):
-    """_vec of at least n contiguous fp32 values."""
+    """Pointer of at least n contiguous fp32 values (None -> NULL, integers are raw pointers)."""
     if t is None or type(t) is int:
         return t
     if t.get_device() != dev or t.numel() < n or t.element_size() != 4 or not t.is_contiguous():
@@ -599,8 +590,14 @@ def _meta(t, o, k, dev):
     return t if t is None else _packed(t, (k + 127) // 128 * o * 16, dev)
 
 
-def _bytes(t):
-    return 0 if t is None or type(t) is int else t.numel() * t.element_size()
+def _scratch(t, size, dev):
+    """(pointer, bytes) of a workspace; size: None, or a part of it to use."""
+    if t is None or type(t) is int:
+        return t, size or 0
+    have = t.numel() * t.element_size()
+    if t.get_device() != dev or not t.is_contiguous() or (size is not None and size > have):
+        _refuse(t, dev, "a contiguous workspace of at least the stated bytes is needed")
+    return t.data_ptr(), have if size is None else size
 
 
 def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, ldx=None, ldq=None, check=True):
@@ -670,11 +667,11 @@ def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift
     xp, lx = _codes(x, sx, dev, t, k, ldx)
     wp, lw = _codes(w, sw, dev, o, k if w_meta is None else k // 2, ldw)
     yp, ly, yd = _i8_out(y, t, o, dev, ldy, y_dtype)
+    wsp, wsn = _scratch(workspace, workspace_bytes, dev)
     st = lib().nm_spmm_i8(xp, t, k, lx, _factors(x_scale, t, dev), wp, o,
                           lw, _factors(w_scale, o, dev), _meta(w_meta, o, k, dev),
                           _factors(row_shift, t, dev), _factors(col_shift, o, dev), yp, ly, yd, accumulate,
-                          _vec(workspace, dev), _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
-                          ctypes.addressof(taken) if taken is not None else None, _stream(stream))
+                          wsp, wsn, route, ctypes.addressof(taken) if taken is not None else None, _stream(stream))
     if check and st:
         _check(st, "nm_spmm_i8")
     return st
@@ -702,11 +699,11 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
     if lg != lu:
         raise ValueError("w_gate and w_up need the same leading dimension")
     yp, ly, yd = _i8_out(y, t, inter, dev, ldy, y_dtype)
+    wsp, wsn = _scratch(workspace, workspace_bytes, dev)
     st = lib().nm_glu_i8(xp, t, k, lx, _factors(x_scale, t, dev), gp,
                          _factors(gate_scale, inter, dev), _meta(gate_meta, inter, k, dev), up,
                          _factors(up_scale, inter, dev), _meta(up_meta, inter, k, dev), inter, lg, act, yp, ly, yd,
-                         _vec(workspace, dev), _bytes(workspace) if workspace_bytes is None else workspace_bytes, route,
-                         ctypes.addressof(taken) if taken is not None else None, _stream(stream))
+                         wsp, wsn, route, ctypes.addressof(taken) if taken is not None else None, _stream(stream))
     if check and st:
         _check(st, "nm_glu_i8")
     return st

@@ -177,3 +177,18 @@ def test_products_refuse_outputs_written_past_their_end(calls, call):
     a = taken(calls, call, x, w, 1 << 20, o=8, ldy=8, y_dtype=S.NM_Y_BF16)   # a raw pointer is the caller's
     at = a.index(1 << 20)
     assert a[at + 1:at + 3] == (8, S.NM_Y_BF16)
+
+
+@pytest.mark.parametrize("call", [product, gated])
+def test_products_refuse_workspaces_they_would_write_past(calls, call):
+    x, w, y, ws = i8(4, 64), i8(8, 64), torch.zeros(4, 8), u8(256)
+    refused(calls, call, x, w, y, workspace=u8(512)[::2])                    # every second byte is someone else's
+    refused(calls, call, x, w, y, workspace=u8(16, 32)[:, :16])
+    refused(calls, call, x, w, y, workspace=ws, workspace_bytes=257)
+    for kw, size in (({}, 256), ({"workspace_bytes": 64}, 64), ({"workspace": torch.zeros(64)}, 256),
+                     ({"workspace": 1 << 20, "workspace_bytes": 512}, 512), ({"workspace": 1 << 20}, 0),
+                     ({"workspace": None}, 0)):
+        kw = {"workspace": ws, **kw}
+        a = taken(calls, call, x, w, y, **kw)
+        p = kw["workspace"]
+        assert a[-5:-3] == (p.data_ptr() if torch.is_tensor(p) else p, size)
