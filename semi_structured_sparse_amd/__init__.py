@@ -656,7 +656,8 @@ def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift
     """y = (x . w^T) * x_scale * w_scale (+ row_shift * col_shift) in 8-bit integers; w_meta (from
     nm_meta_block): 2:4 weights.  k: the reduction length where it is not x's width.
     taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
-    dev = _device() if stream is None else _device_of(x, w, y)
+    dev = _device() if stream is None else _device_of(x, w, y, x_scale, w_scale, w_meta, row_shift, col_shift,
+                                                                   workspace)
     sx, sw = _shape(x), _shape(w)
     if t is None:
         t = sx[0]
@@ -682,7 +683,8 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
               workspace_bytes=None, route=0, taken=None, check=True):
     """y = act(x . w_gate^T) * (x . w_up^T), each with its scales, in 8-bit integers.
     taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
-    dev = _device() if stream is None else _device_of(x, w_gate, y)
+    dev = _device() if stream is None else _device_of(x, w_gate, y, w_up, x_scale, gate_scale, up_scale, gate_meta,
+                                                                   up_meta, workspace)
     sx, sg, su = _shape(x), _shape(w_gate), _shape(w_up)
     if t is None:
         t = sx[0]

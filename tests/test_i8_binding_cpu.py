@@ -192,3 +192,24 @@ def test_products_refuse_workspaces_they_would_write_past(calls, call):
         a = taken(calls, call, x, w, y, **kw)
         p = kw["workspace"]
         assert a[-5:-3] == (p.data_ptr() if torch.is_tensor(p) else p, size)
+
+
+# ------------------------------------------------------------------- raw pointers and tensors ---
+
+def test_tensors_beside_raw_pointers_on_a_named_stream(calls, monkeypatch):
+    """With the stream given, tensors count wherever they stand among raw pointers."""
+    class OnGpu(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    monkeypatch.setattr(S, "_current_device", lambda: 0)
+    gpu = lambda t: t.as_subclass(OnGpu)  # noqa: E731
+    one, p = gpu(torch.ones(64)), 1 << 20
+    taken(calls, S.nm_spmm_i8, p, one, p, p, p, stream=0, t=4, o=8, k=64, ldx=64, ldw=64, ldy=8)
+    taken(calls, S.nm_spmm_i8, p, p, p, p, p, p, None, one, stream=0, t=4, o=8, k=64, ldx=64, ldw=64, ldy=8)
+    taken(calls, S.nm_spmm_i8, p, p, p, p, p, gpu(u8(128)), stream=0, t=4, o=8, k=64, ldx=64, ldw=64, ldy=8)
+    taken(calls, S.nm_spmm_i8, p, p, p, p, p, workspace=gpu(u8(64)), stream=0, t=4, o=8, k=64, ldx=64, ldw=64, ldy=8)
+    taken(calls, S.nm_glu_i8, p, p, p, p, p, one, p, stream=0, t=4, inter=8, k=64, ldx=64, ldw=64, ldy=8)
+    taken(calls, S.nm_glu_i8, p, p, p, p, gpu(i8(8, 64)), p, p, stream=0, t=4, inter=8, k=64, ldx=64, ldw=64, ldy=8)
+    refused(calls, S.nm_spmm_i8, p, torch.ones(64), p, p, p, stream=0, t=4, o=8, k=64, ldx=64, ldw=64, ldy=8)   # on the CPU
+    refused(calls, S.nm_spmm_i8, p, one, p, torch.ones(64), p, stream=0, t=4, o=8, k=64, ldx=64, ldw=64, ldy=8)
