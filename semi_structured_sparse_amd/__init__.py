@@ -545,7 +545,7 @@ def _codes(m, sh, dev, rows, cols, ld):
     if len(st) != 2 or st[1] != 1 or m.get_device() != dev or m.element_size() != 1:
         _refuse(m, dev, "a matrix with contiguous rows of 1-byte elements is needed")
     if ld is None:
-        ld = st[0]
+        ld = st[0] if cols else 0       # of no columns: torch has 1
     if sh[0] < rows or sh[1] < cols + -cols % 16 or ld != st[0]:
         _holds(m, rows, cols, 16, ld)
     return m.data_ptr(), ld
@@ -605,6 +605,8 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
     dev = _device() if stream is None else _device_of(x, q, scale)
     xp, lx = _mat(x, dev, 2)
     qp, lq = _mat(q, dev, 1)
+    if ldx is not None:
+        lx = ldx
     if ldq is not None:
         lq = ldq
     if xp is not x:                      # a tensor
@@ -618,7 +620,7 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
         if width < k:
             raise ValueError(f"x of rows of {k} values is needed")
         if have < rows or width & 7 or ldx is not None:
-            _holds(x, rows, k, 8, lx if ldx is None else ldx)
+            _holds(x, rows, k, 8, lx)
     if qp is not q:
         have, width = q.shape
         kq = k // (2 * ns) * 4 * (ns - 1) if ns > 2 else k
@@ -626,7 +628,9 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
             raise ValueError(f"q of rows of {kq} codes is needed")
         if have < rows or width & 15 or ldq is not None:
             _holds(q, rows, kq, 16, lq)
-    st = lib().nm_quant_i8(xp, rows, k, lx if ldx is None else ldx, n, m, ns, qp, lq, _factors(scale, rows, dev),
+    if k == 0:                           # torch has a leading dimension of 1 for no columns
+        lx, lq = ldx or 0, ldq or 0
+    st = lib().nm_quant_i8(xp, rows, k, lx, n, m, ns, qp, lq, _factors(scale, rows, dev),
                            _stream(stream))
     if check and st:
         _check(st, "nm_quant_i8")

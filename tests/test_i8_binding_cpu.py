@@ -213,3 +213,24 @@ def test_tensors_beside_raw_pointers_on_a_named_stream(calls, monkeypatch):
     taken(calls, S.nm_glu_i8, p, p, p, p, gpu(i8(8, 64)), p, p, stream=0, t=4, inter=8, k=64, ldx=64, ldw=64, ldy=8)
     refused(calls, S.nm_spmm_i8, p, torch.ones(64), p, p, p, stream=0, t=4, o=8, k=64, ldx=64, ldw=64, ldy=8)   # on the CPU
     refused(calls, S.nm_spmm_i8, p, one, p, torch.ones(64), p, stream=0, t=4, o=8, k=64, ldx=64, ldw=64, ldy=8)
+
+
+# ----------------------------------------------------------------------------- empty rows ---
+
+def test_rows_of_no_values(calls):
+    """torch gives a matrix of no columns the leading dimension 1, which no alignment rule takes."""
+    a = taken(calls, S.nm_quant_i8, bf16(4, 0), i8(4, 0), torch.zeros(4))
+    assert a[1:4] == (4, 0, 0) and a[8] == 0
+    a = taken(calls, S.nm_quant_i8, bf16(4, 64), i8(4, 64), torch.zeros(4), k=0)
+    assert a[1:4] == (4, 0, 0) and a[8] == 0
+    for call in (product, gated):
+        a = taken(calls, call, i8(4, 0), i8(8, 0), torch.zeros(4, 8))
+        assert a[1:4] == (4, 0, 0) and 1 not in a[:14]
+        a = taken(calls, call, i8(4, 64), i8(8, 64), torch.zeros(4, 8), k=0)
+        assert a[1:4] == (4, 0, 0)
+
+
+def test_rows_of_no_values_are_valid():
+    """The library itself (nothing to launch: no rows)."""
+    assert S.lib().nm_quant_i8(None, 0, 0, 0, 0, 0, 2, None, 0, None, None) == S.NM_OK
+    assert S.lib().nm_quant_i8(None, 0, 0, 1, 0, 0, 2, None, 0, None, None) == S.NM_EALIGN
