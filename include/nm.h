@@ -603,6 +603,8 @@ typedef enum { NM_Y_F32 = 0, NM_Y_BF16 = 1 } nm_ydtype;
 /*
  * nm_spmm_i8 -- the linear layer in 8-bit integers:
  *   Y[t][o] (=|+=) (fp32(sum_k x[t][k] w[o][k]) * x_scale[t]) * w_scale[o] + beta_t * col_shift[o]
+ *            rounded to fp32 after fp32(), after each scale, once for the term's product and sum
+ *            together (fused), and once for an accumulation
  *   x        int8 [t][ldx], x_scale fp32 [t]  (nm_quant_i8 of the activations; lifted codes and
  *            k = K' for lowered weights)
  *   w        w_meta NULL: int8 [o][ldw], dense, any k.  Otherwise 2:4 over k (k % 4 == 0): the

@@ -238,8 +238,9 @@ __global__ __launch_bounds__(256) void k_i8_reduce(const int32_t* __restrict__ p
   f32x4 v;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    if (!GLU && !shifted) v[r] = ((float)s0[r] * xs) * ws[r];
-    else v[r] = i8_value<GLU>(epi, s0[r], s1[r], xs, ws[r], es[r], rb, es[r]);
+    if constexpr (GLU) v[r] = i8_gated(epi, s0[r], s1[r], xs, ws[r], es[r]);
+    else v[r] = i8_scaled(s0[r], xs, ws[r]);
+    if (shifted) v[r] = i8_shifted(v[r], rb, es[r]);
   }
   if (epi.bf16_out) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(epi.y) + t * epi.ldy + o) =

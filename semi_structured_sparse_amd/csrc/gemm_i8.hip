@@ -190,12 +190,12 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int s0 = acc[GLU ? 2 * i : i][j][r], s1 = GLU ? acc[GLU ? 2 * i + 1 : i][j][r] : 0;
-      if constexpr (GLU) v[r] = i8_value<GLU>(epi, s0, s1, xs[j], sc.w[r], sc.e[r], rb[j], sc.e[r]);
-      else v[r] = ((float)s0 * xs[j]) * sc.w[r];
+      if constexpr (GLU) v[r] = i8_gated(epi, s0, s1, xs[j], sc.w[r], sc.e[r]);
+      else v[r] = i8_scaled(s0, xs[j], sc.w[r]);
     }
     if (shifted) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] += rb[j] * sc.e[r];
+      for (int r = 0; r < 4; ++r) v[r] = i8_shifted(v[r], rb[j], sc.e[r]);
     }
     return v;
   };
@@ -655,9 +655,9 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
             const int s0 = acc_read(blk[4 * g + r]);
             if constexpr (GLU) {
               const int s1 = acc_read(blk[8 + 4 * g + r]);
-              v[b][g][r] = i8_value<true>(epi, s0, s1, xs[j], ws[b][g][r], es[b][g][r], 0.f, 0.f);
+              v[b][g][r] = i8_gated(epi, s0, s1, xs[j], ws[b][g][r], es[b][g][r]);
             } else {
-              v[b][g][r] = ((float)s0 * xs[j]) * ws[b][g][r];
+              v[b][g][r] = i8_scaled(s0, xs[j], ws[b][g][r]);
             }
           }
       if (shifted) {
@@ -666,7 +666,7 @@ __device__ __forceinline__ void i8_finish_big(const i32x16 (&acc)[4][4], const I
 #pragma unroll
           for (int g = 0; g < NG; ++g)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[b][g][r] += rb[j] * es[b][g][r];
+            for (int r = 0; r < 4; ++r) v[b][g][r] = i8_shifted(v[b][g][r], rb[j], es[b][g][r]);
       }
       const int64_t tj = tb_w + 32 * j;
       if (epi.bf16_out) {

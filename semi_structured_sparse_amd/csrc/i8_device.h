@@ -3,6 +3,11 @@
 #include "i8_launch.h"
 #include "nm_device.h"
 
+// Roundings are the ones written in these files: no product is fused into a sum unless it says
+// fmaf.  (Left to the compiler, the shift's product, the scale's product or the accumulation
+// could be fused in one kernel and not in another, and routes would give other bits.)
+#pragma clang fp contract(off)
+
 namespace nmk {
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
@@ -28,7 +33,7 @@ __device__ __forceinline__ void wave_lds_fence() {
 // 1/4, so that the reciprocal, which has no subnormal results, covers every finite exponential.
 __device__ __forceinline__ float glu_gate(float g, int act) {
   float z = g;
-  if (act == NM_GLU_GELU_TANH) z = 1.5957691216057308f * (g + 0.044715f * (g * g * g));
+  if (act == NM_GLU_GELU_TANH) z = 1.5957691216057308f * __builtin_fmaf(0.044715f, g * g * g, g);
   const float d = 0.25f + __builtin_amdgcn_exp2f(__builtin_fmaf(z, -1.442695041f, -2.0f));
   return (0.25f * fmaxf(g, -3.402823466e38f)) * __builtin_amdgcn_rcpf(d);
 }
@@ -40,25 +45,26 @@ __device__ __forceinline__ uint16_t bf16_rne(float v) {
   return (uint16_t)((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
 }
 
-// The value of one output from its sums (s1: the second weight's, GLU).
-template <bool GLU>
-__device__ __forceinline__ float i8_value(const nml::I8Epi& e, int s0, int s1, float xs, float ws, float us, float rb,
-                                          float cs) {
-  const float v = ((float)s0 * xs) * ws;
-  if constexpr (GLU) return glu_gate(v, e.act) * (((float)s1 * xs) * us);
-  return v + rb * cs;
+// A sum with its scales, and the shift term added to it: the steps of every epilogue.
+__device__ __forceinline__ float i8_scaled(int s, float xs, float ws) { return ((float)s * xs) * ws; }
+__device__ __forceinline__ float i8_shifted(float v, float rb, float cs) { return __builtin_fmaf(rb, cs, v); }
+
+// The value of one GLU output from its sums (s1: the second weight's).
+__device__ __forceinline__ float i8_gated(const nml::I8Epi& e, int s0, int s1, float xs, float ws, float us) {
+  return glu_gate(i8_scaled(s0, xs, ws), e.act) * i8_scaled(s1, xs, us);
 }
 
 // One output, every address worked out (the few-token kernels and the reduction).
 template <bool GLU>
 __device__ __forceinline__ void i8_store(const nml::I8Epi& e, int s0, int s1, int64_t t, int64_t o) {
-  const float cs = !GLU && e.col_shift != nullptr ? e.col_shift[o] : 0.f;
-  const float rb = !GLU && e.row_shift != nullptr ? e.row_shift[t] : 1.f;
-  const float ws = e.w_scale[o], us = GLU ? e.up_scale[o] : 0.f;
-  const float xs = e.x_scale[t];
+  const float xs = e.x_scale[t], ws = e.w_scale[o];
   float v;
-  if (!GLU && e.col_shift == nullptr) v = ((float)s0 * xs) * ws;
-  else v = i8_value<GLU>(e, s0, s1, xs, ws, us, rb, cs);
+  if constexpr (GLU) {
+    v = i8_gated(e, s0, s1, xs, ws, e.up_scale[o]);
+  } else {
+    v = i8_scaled(s0, xs, ws);
+    if (e.col_shift != nullptr) v = i8_shifted(v, e.row_shift != nullptr ? e.row_shift[t] : 1.f, e.col_shift[o]);
+  }
   if (e.bf16_out) {
     static_cast<uint16_t*>(e.y)[t * e.ldy + o] = bf16_rne(v);
   } else {
