@@ -5,10 +5,8 @@ import numpy as np
 import pytest
 
 import oracle as O
-import synth
 from nm_testutil import dev
-from test_i8_gpu import (ROUTES, Guarded, build_mlp, check_glu, check_mlp, check_product, make_weight, mlp,
-                         random_codes, sync, up, ws_for)
+from test_i8_gpu import ROUTES, Guarded, check_glu, check_product, make_weight, random_codes, sync, up, ws_for
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +50,81 @@ def test_outputs_have_the_documented_roundings(sparse, ldy_extra):
                              dev(rb) if shift else None, dev(cs) if shift else None, acc, ws_for(t, o, k, sparse, False, r),
                              t=t, o=o, k=k, route=r)
                 assert np.array_equal(g.get(), want.astype(np.float64)), (t, o, k, shift, acc, name)
+
+
+# ---------------------------------------------------------------- tile shapes and splits ---
+# Sizes by the rule of the smaller tiles: the largest of 128 x 128, 128 x 64, 64 x 64, 64 x 32 (weight
+# rows x tokens; a GLU tile has half as many outputs) that gives 192 workgroups.
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("sparse", [False, True])
+def test_glu_on_128_by_128_tiles(sparse, act):
+    rng = np.random.default_rng(120 + sparse)
+    for t, o, k in [(128, 12992, 256), (250, 6530, 132), (190, 7001, 644)]:
+        check_glu(rng, t, o, k, sparse, act, routes=("auto", "split"))
+        check_glu(rng, t, o, k, sparse, act, routes=("split",), bf16=True, ldy=up(o, 8))
+        check_glu(rng, t, o, k, sparse, act, routes=("split",), bf16=True, ldy=o + 1 - o % 2)
+    check_glu(rng, 128, 12403, 128, sparse, act, routes=("split",), ldy=12403)
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_products_on_128_by_128_and_128_by_64_tiles(sparse):
+    rng = np.random.default_rng(124 + sparse)
+    for t, o, k in [(300, 8300, 260), (1000, 3202, 644), (90, 13001, 388), (64, 25001, 128)]:
+        for bf16, shift, acc in [(True, 0, 0), (True, 1, 0), (False, 2, 0), (False, 0, 1), (False, 2, 1)]:
+            check_product(rng, t, o, k, sparse, routes=("split",), bf16=bf16, shift=shift, accumulate=acc, ldy=o + 1 - o % 2)
+            check_product(rng, t, o, k, sparse, routes=("split",), bf16=bf16, shift=shift, accumulate=acc, ldy=up(o, 8))
+
+
+def in_two(t, o, k, sparse, glu):
+    """The call's reduction is cut in two ranges (two partial sums of every output)."""
+    return S.nm_i8_workspace_size(t, o, k, sparse, glu) == 2 * (2 if glu else 1) * t * up(o, 4) * 4
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_products_of_long_reductions_in_two_ranges(sparse):
+    """64 x 64 tiles twice where 64 x 32 tiles would have over 64 steps."""
+    rng = np.random.default_rng(128 + sparse)
+    for t, o, k in [(100, 4100, 8320), (70, 4221, 8324), (40, 6300, 8448)]:
+        assert in_two(t, o, k, sparse, False)
+        check_product(rng, t, o, k, sparse, routes=("auto", "stream", "tile"))
+        check_product(rng, t, o, k, sparse, bf16=True, shift=1, ldy=up(o, 8))
+        check_product(rng, t, o, k, sparse, bf16=True, shift=2, ldy=o + 1 - o % 2)
+        check_product(rng, t, o, k, sparse, shift=2, accumulate=1, ldy=up(o, 4))
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_glu_of_long_reductions_in_two_ranges(sparse):
+    rng = np.random.default_rng(132 + sparse)
+    for t, o, k in [(100, 2100, 8320), (70, 2221, 8324)]:
+        assert in_two(t, o, k, sparse, True)
+        check_glu(rng, t, o, k, sparse, "silu", routes=("auto", "stream", "tile"))
+        check_glu(rng, t, o, k, sparse, "gelu", bf16=True, ldy=up(o, 8))
+        check_glu(rng, t, o, k, sparse, "gelu", bf16=True, ldy=o + 1 - o % 2)
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_more_tiles_give_the_same_bits_every_time(sparse):
+    """128 x 64 tiles, GLU tiles of each size, and reductions in ranges, call after call."""
+    rng = np.random.default_rng(136 + sparse)
+    for t, o, k, glu in [(500, 3300, 2048, False), (100, 4100, 8320, False), (61, 1024, 8192, False), (250, 6530, 1024, True),
+                         (500, 1700, 2048, True), (100, 3300, 2048, True), (100, 2100, 8320, True)]:
+        x = torch.from_numpy(random_codes(rng, t, k, k, True)).cuda()
+        w0, m0, s0, _ = make_weight(rng, o, k, sparse)
+        w1, m1, s1, _ = make_weight(rng, o, k, sparse)
+        xs, s0, s1 = torch.full((t,), 1 / 4096, device="cuda"), dev(s0), dev(s1)
+        want, y = (torch.empty(t, o + 1, device="cuda") for _ in range(2))
+
+        def run(out, route):
+            ws = ws_for(t, o, k, sparse, glu, route)
+            if glu:
+                S.nm_glu_i8(x, xs, w0, s0, w1, s1, out, S.NM_GLU_SILU, m0, m1, ws, k=k, inter=o, route=route)
+            else:
+                S.nm_spmm_i8(x, xs, w0, s0, out, m0, workspace=ws, k=k, o=o, route=route)
+
+        run(want, ROUTES["stream"])
+        for i in range(60):
+            y.fill_(float("nan"))
+            run(y, ROUTES["split" if i % 4 else "tile"])
+            sync()
+            assert torch.equal(y[:, :o], want[:, :o]), (t, o, k, glu, i)
