@@ -5,8 +5,10 @@ import numpy as np
 import pytest
 
 import oracle as O
+import synth
 from nm_testutil import dev
-from test_i8_gpu import ROUTES, Guarded, check_glu, check_product, make_weight, random_codes, sync, up, ws_for
+from test_i8_gpu import (ROUTES, Guarded, build_mlp, check_glu, check_mlp, check_product, make_weight, mlp,
+                         random_codes, sync, up, ws_for)
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +130,68 @@ def test_more_tiles_give_the_same_bits_every_time(sparse):
             run(y, ROUTES["split" if i % 4 else "tile"])
             sync()
             assert torch.equal(y[:, :o], want[:, :o]), (t, o, k, glu, i)
+
+
+# ------------------------------------------------------------- split runs in a served MLP ---
+
+def both_split(t, hid, inter):
+    return [S.nm_i8_workspace_size(t, inter, hid, True, True) > 0, S.nm_i8_workspace_size(t, hid, inter, False, False) > 0]
+
+
+# the down product in eight ranges, the gate and up products in four, the down product in two
+SPLIT_MLPS = [(24, 256, 16384, [False, True]), (24, 8192, 256, [True, False]), (100, 4112, 8448, [False, True])]
+
+
+@pytest.mark.parametrize("t,hid,inter,split", SPLIT_MLPS)
+def test_split_mlp_captured_and_replayed(t, hid, inter, split):
+    """The whole run with its partial sums and their second kernel in one graph, replayed with new
+    inputs, eager work in between."""
+    assert both_split(t, hid, inter) == split
+    rng = np.random.default_rng(140)
+    bufs, weights = build_mlp(rng, t, hid, inter, False)
+    xs = [dev(synth.normal_bf16(rng, (t, hid))) for _ in range(3)]
+    xd = xs[0].clone()
+    eager = []
+    for x in xs:
+        xd.copy_(x)
+        mlp(xd, False, t, hid, inter, bufs)
+        eager.append(bufs["y"].clone())
+    sync()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mlp(xd, False, t, hid, inter, bufs)
+    for i in (0, 1, 2, 1, 0):
+        xd.copy_(xs[i])
+        bufs["y"].fill_(float("nan"))
+        bufs["ws"].fill_(0x55)
+        g.replay()
+        sync()
+        assert torch.equal(bufs["y"], eager[i])
+        torch.randn(100, 100, device="cuda").sum().item()
+    if inter * hid < 1 << 23:
+        check_mlp(bufs, xs[0].cpu().numpy().view(np.uint16), weights, False)
+
+
+@pytest.mark.parametrize("t,hid,inter,split", SPLIT_MLPS)
+def test_split_mlps_on_two_streams_at_once(t, hid, inter, split):
+    """Two streams, each with its own buffers and partial sums, give what one after the other gives."""
+    assert both_split(t, hid, inter) == split
+    rng = np.random.default_rng(144)
+    sets = [build_mlp(rng, t, hid, inter, False)[0] for _ in range(2)]
+    xs = [dev(synth.normal_bf16(rng, (t, hid))) for _ in range(2)]
+    want = []
+    for b, x in zip(sets, xs):
+        mlp(x, False, t, hid, inter, b)
+        sync()
+        want.append(b["y"].clone())
+        b["y"].zero_()
+    assert not torch.equal(want[0], want[1])
+    sync()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for b, x, s in zip(sets, xs, streams):
+            with torch.cuda.stream(s):
+                mlp(x, False, t, hid, inter, b)
+    sync()
+    for b, w in zip(sets, want):
+        assert torch.equal(b["y"], w)
