@@ -194,7 +194,7 @@ def _ld(t, default=0):
     return default
 
 
-_current_raw_stream = None      # () -> raw current stream of the current device
+_current_raw_stream = None      # device -> raw current stream
 _current_device = None          # () -> the current device
 _half = None                    # torch.float16, which the int8 layers refuse where bf16 is meant
 
@@ -207,24 +207,24 @@ def _bind_torch():
     raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
     # building a Stream object costs 2.7 us a call, the raw handle 0.2 us (one-token calls take 6)
     if raw is not None and device is not None:
-        _current_raw_stream, _current_device = (lambda: raw(device())), device
+        _current_raw_stream, _current_device = raw, device
     else:
-        _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        _current_raw_stream = lambda dev: torch.cuda.current_stream(dev).cuda_stream  # noqa: E731
         _current_device = torch.cuda.current_device
+
+
+def _current():
+    """(current device, its raw current stream)"""
+    if _current_raw_stream is None:
+        _bind_torch()
+    dev = _current_device()
+    return dev, _current_raw_stream(dev)
 
 
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    if _current_raw_stream is None:
-        _bind_torch()
-    return _current_raw_stream()
-
-
-def _device():
-    if _current_device is None:
-        _bind_torch()
-    return _current_device()
+    return _current()[1]
 
 
 def _check(status: int, where: str):
@@ -500,7 +500,7 @@ def _device_of(*ts):
         if t is not None and type(t) is not int:
             if t.get_device() < 0:
                 _refuse(t, 0, "")
-            return _device()
+            return _current()[0]
     return -1
 
 
@@ -532,10 +532,6 @@ def _holds(t, rows, cols, whole, ld):
             raise ValueError(f"the storage ends inside the last of {rows} rows of {cols} elements, {ld} apart")
 
 
-def _shape(t):
-    return None if t is None or type(t) is int else t.shape
-
-
 def _codes(m, sh, dev, rows, cols, ld):
     """(pointer, leading dimension) of int8 codes of shape sh that are read: `rows` rows of `cols`, in
     pieces of 16; ld: None, or a leading dimension in place of the tensor's."""
@@ -555,7 +551,7 @@ def _factors(t, n, dev):
     """Pointer of at least n contiguous fp32 values (None -> NULL, integers are raw pointers)."""
     if t is None or type(t) is int:
         return t
-    if t.get_device() != dev or t.numel() < n or t.element_size() != 4 or not t.is_contiguous():
+    if t.get_device() != dev or t.nbytes < 4 * n or t.element_size() != 4 or not t.is_contiguous():
         _refuse(t, dev, f"{n} contiguous fp32 factors are needed")
     return t.data_ptr()
 
@@ -580,7 +576,7 @@ def _packed(t, size, dev):
     """Pointer of at least `size` contiguous bytes of positions."""
     if t is None or type(t) is int:
         return t
-    if t.get_device() != dev or t.numel() * t.element_size() < size or not t.is_contiguous():
+    if t.get_device() != dev or t.nbytes < size or not t.is_contiguous():
         _refuse(t, dev, f"{size} contiguous bytes of positions are needed")
     return t.data_ptr()
 
@@ -594,7 +590,7 @@ def _scratch(t, size, dev):
     """(pointer, bytes) of a workspace; size: None, or a part of it to use."""
     if t is None or type(t) is int:
         return t, size or 0
-    have = t.numel() * t.element_size()
+    have = t.nbytes
     if t.get_device() != dev or not t.is_contiguous() or (size is not None and size > have):
         _refuse(t, dev, "a contiguous workspace of at least the stated bytes is needed")
     return t.data_ptr(), have if size is None else size
@@ -602,7 +598,10 @@ def _scratch(t, size, dev):
 
 def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, ldx=None, ldq=None, check=True):
     """Rows of bf16 x -> int8 codes q and one fp32 scale per row (include/nm.h)."""
-    dev = _device() if stream is None else _device_of(x, q, scale)
+    if stream is None:
+        dev, stream = _current()
+    else:
+        dev, stream = _device_of(x, q, scale), _stream(stream)
     xp, lx = _mat(x, dev, 2)
     qp, lq = _mat(q, dev, 1)
     if ldx is not None:
@@ -631,7 +630,7 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
     if k == 0:                           # torch has a leading dimension of 1 for no columns
         lx, lq = ldx or 0, ldq or 0
     st = lib().nm_quant_i8(xp, rows, k, lx, n, m, ns, qp, lq, _factors(scale, rows, dev),
-                           _stream(stream))
+                           stream)
     if check and st:
         _check(st, "nm_quant_i8")
     return st
@@ -639,8 +638,11 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
 
 def nm_meta_block(meta, o, kc, out, stream=None, *, check=True):
     """2-bit positions in rows -> step blocks (include/nm.h); both tensors contiguous."""
-    dev = _device() if stream is None else _device_of(meta, out)
-    st = lib().nm_meta_block(_packed(meta, o * ((kc + 7) // 8), dev), o, kc, _meta(out, o, kc, dev), _stream(stream))
+    if stream is None:
+        dev, stream = _current()
+    else:
+        dev, stream = _device_of(meta, out), _stream(stream)
+    st = lib().nm_meta_block(_packed(meta, o * ((kc + 7) // 8), dev), o, kc, _meta(out, o, kc, dev), stream)
     if check:
         _check(st, "nm_meta_block")
     return st
@@ -660,9 +662,12 @@ def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift
     """y = (x . w^T) * x_scale * w_scale (+ row_shift * col_shift) in 8-bit integers; w_meta (from
     nm_meta_block): 2:4 weights.  k: the reduction length where it is not x's width.
     taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
-    dev = _device() if stream is None else _device_of(x, w, y, x_scale, w_scale, w_meta, row_shift, col_shift,
-                                                                   workspace)
-    sx, sw = _shape(x), _shape(w)
+    if stream is None:
+        dev, stream = _current()
+    else:
+        dev, stream = _device_of(x, w, y, x_scale, w_scale, w_meta, row_shift, col_shift, workspace), _stream(stream)
+    sx = None if x is None or type(x) is int else x.shape
+    sw = None if w is None or type(w) is int else w.shape
     if t is None:
         t = sx[0]
     if o is None:
@@ -676,7 +681,7 @@ def nm_spmm_i8(x, x_scale, w, w_scale, y, w_meta=None, row_shift=None, col_shift
     st = lib().nm_spmm_i8(xp, t, k, lx, _factors(x_scale, t, dev), wp, o,
                           lw, _factors(w_scale, o, dev), _meta(w_meta, o, k, dev),
                           _factors(row_shift, t, dev), _factors(col_shift, o, dev), yp, ly, yd, accumulate,
-                          wsp, wsn, route, ctypes.addressof(taken) if taken is not None else None, _stream(stream))
+                          wsp, wsn, route, ctypes.addressof(taken) if taken is not None else None, stream)
     if check and st:
         _check(st, "nm_spmm_i8")
     return st
@@ -687,9 +692,14 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
               workspace_bytes=None, route=0, taken=None, check=True):
     """y = act(x . w_gate^T) * (x . w_up^T), each with its scales, in 8-bit integers.
     taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
-    dev = _device() if stream is None else _device_of(x, w_gate, y, w_up, x_scale, gate_scale, up_scale, gate_meta,
-                                                                   up_meta, workspace)
-    sx, sg, su = _shape(x), _shape(w_gate), _shape(w_up)
+    if stream is None:
+        dev, stream = _current()
+    else:
+        dev, stream = _device_of(x, w_gate, y, w_up, x_scale, gate_scale, up_scale, gate_meta,
+                                up_meta, workspace), _stream(stream)
+    sx = None if x is None or type(x) is int else x.shape
+    sg = None if w_gate is None or type(w_gate) is int else w_gate.shape
+    su = None if w_up is None or type(w_up) is int else w_up.shape
     if t is None:
         t = sx[0]
     if inter is None:
@@ -709,7 +719,7 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
     st = lib().nm_glu_i8(xp, t, k, lx, _factors(x_scale, t, dev), gp,
                          _factors(gate_scale, inter, dev), _meta(gate_meta, inter, k, dev), up,
                          _factors(up_scale, inter, dev), _meta(up_meta, inter, k, dev), inter, lg, act, yp, ly, yd,
-                         wsp, wsn, route, ctypes.addressof(taken) if taken is not None else None, _stream(stream))
+                         wsp, wsn, route, ctypes.addressof(taken) if taken is not None else None, stream)
     if check and st:
         _check(st, "nm_glu_i8")
     return st

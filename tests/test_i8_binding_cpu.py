@@ -24,7 +24,7 @@ def calls(monkeypatch):
     rec = Recorder()
     monkeypatch.setattr(S, "lib", lambda: rec)
     monkeypatch.setattr(S, "_current_device", lambda: -1)
-    monkeypatch.setattr(S, "_current_raw_stream", lambda: 0)
+    monkeypatch.setattr(S, "_current_raw_stream", lambda dev: 0)
     monkeypatch.setattr(S, "_half", torch.float16)
     return rec.calls
 
