@@ -50,16 +50,31 @@ enum class Kind { kFew, kMid, kLarge };
 
 // Up to 32 tokens the streaming kernel, whose row blocks need no partial sums, unless 64 x 32
 // tiles fill the chip unsplit (192 of them) or X, which every row block of the streaming kernel
-// reads again, is long.  Measured (us, streaming / tiles): dense 1 x 4096 x 4096 5.3 / 7.3,
-// 16 x 4096 x 4096 6.7 / 8.2, 32 x 4096 x 4096 8.8 / 9.0, 8 x 4096 x 14336 13.3 / 14.2,
-// 16 x 4096 x 14336 15.6 / 14.6, 32 x 4096 x 14336 22.0 / 15.1, 1 x 14336 x 4096 12.5 / 10.8,
-// 16 x 14336 x 4096 14.4 / 11.5; 2:4 1 x 4096 x 14336 9.7 / 11.5, 16 x 4096 x 14336 14.4 / 12.2,
-// 16 x 14336 x 4096 11.6 / 8.7.  Above, 256 x 256 tiles from 160 of them, smaller tiles below.
-// Measured (us, smaller / 256 x 256; tiles): dense 2048 x 4096 x 4096 40 / 48 (128), 2048 x 4096 x
-// 14336 112 / 145 (128), 700 x 14336 x 1024 24 / 19 (168), 3000 x 4096 x 2048 35 / 29 (192), GLU
-// 1536 x 4096 x 14336 196 / 162 (192), 1024 x 14336 x 4096 74 / 52 (224); 2:4 512 x 14336 x 4096
-// 31 / 35 (112), 2048 x 4096 x 4096 32 / 34 (128), 2048 x 4096 x 14336 94 / 91 (128), 700 x 14336 x
-// 1024 20 / 18 (168), GLU 256 x 14336 x 4096 30 / 35 (112), 512 x 14336 x 4096 56 / 42 (224).
+// reads again, is long.  Measured (us, streaming / tiles, weights in the 256 MB last-level cache;
+// then the same with weights from HBM): dense 1 x 4096 x 4096 5.9 / 7.9; 6.6 / 10.9, 16 x 4096 x
+// 4096 7.0 / 8.1; 7.8 / 11.2, 32 x 4096 x 4096 8.9 / 8.3; 9.9 / 11.5, 8 x 4096 x 14336 13.5 / 14.2;
+// 15.6 / 16.2, 16 x 4096 x 14336 15.7 / 14.6; 18.6 / 16.4, 32 x 4096 x 14336 22.1 / 15.0; 27.3 /
+// 16.8, 1 x 14336 x 4096 12.5 / 10.8; 17.7 / 15.6, 16 x 14336 x 4096 14.3 / 11.4; 19.4 / 15.3, 16 x
+// 14336 x 256 4.5 / 3.3; 5.3 / 4.0; 2:4 1 x 4096 x 14336 9.8 / 11.5; 11.1 / 14.1, 16 x 4096 x 14336
+// 14.5 / 12.4; 15.7 / 14.4, 16 x 14336 x 4096 11.7 / 8.9; 13.1 / 11.6.
+//
+// Above, 256 x 256 tiles from 160 of them, smaller tiles below, whatever the reduction's length.
+// Measured (us, smaller / 256 x 256; tiles): dense 2048 x 4096 x 4096 40 / 48 (128; weights from HBM
+// 46 / 54), 2048 x 4096 x 14336 112 / 145 (128; 138 / 168), 2100 x 4096 x 14336 173 / 158 (144), 700 x
+// 14336 x 1024 24 / 19 (168), 3000 x 4096 x 2048 35 / 29 (192), 4096 x 4096 x 4096 90 / 60 (256); GLU
+// 1536 x 4096 x 14336 196 / 162 (192), 512 x 14336 x 4096 71 / 54 (224); 2:4 512 x 14336 x 4096 31 /
+// 35 (112), 2048 x 4096 x 4096 32 / 34 (128; 39 / 42), 2048 x 4096 x 14336 94 / 91 (128; 115 / 120),
+// 2100 x 4096 x 14336 143 / 112 (144), 700 x 14336 x 1024 20 / 18 (168), 4096 x 4096 x 4096 75 / 47
+// (256); GLU 256 x 14336 x 4096 30 / 35 (112), 512 x 14336 x 4096 56 / 42 (224).  So the two meet
+// between 128 and 144 tiles, dense and 2:4.
+// Just over a round of 256 tiles the second round is mostly idle and the two are level: 2560 x
+// 7168 x 4096 (280) 99 / 97, 3000 x 6144 x 4096 (288) 98 / 97, 1200 x 14336 x 4096 (280) 98 / 97, 2:4
+// 78 / 76, 78 / 75, 76 / 75; only GLU 600 x 14336 x 4096 (336) loses, 94 / 98, 2:4 71 / 75.
+// Short reductions, 8192 x 4096 over 64, 128, 256, 512, 1024 (512 tiles, fp32 out): dense 41 / 27,
+// 42 / 27, 45 / 31, 50 / 39, 67 / 49, 2:4 31 / 30, 32 / 30, 39 / 33, 49 / 38, 66 / 48; bf16 38 / 18,
+// 38 / 18, 41 / 21, 46 / 28, 63 / 40, 2:4 26 / 22, 27 / 23, 29 / 25, 35 / 31, 47 / 41.  GLU 4096 x
+// 4096 over 128 and 512 35 / 21 and 44 / 31, but 2:4 22 / 26 and 31 / 34: the one kind that smaller
+// tiles would serve better there.
 Kind plan_i8(int64_t t, int64_t o, int64_t k, bool glu, uint32_t route) {
   if (route & NM_ROUTE_FEW_STREAM) return Kind::kFew;
   if (route & NM_ROUTE_FEW_TILE) return Kind::kMid;

@@ -18,10 +18,11 @@
 // bits of positions, and from X the bytes [16 (l / 16), + 16) and [64 + 16 (l / 16), + 16).
 // A step's last pieces may lie past the row: those loads go to sixteen zero bytes instead.
 //
-// Measured (weights from HBM, us, launches of a replayed graph included): 1 x 4096 x 4096 5.3-5.8,
-// 8 x 4096 x 14336 13.3 (4.4 TB/s), 2:4 1 x 4096 x 14336 9.7, GLU 1 x 4096 x 14336 19.8 (5.9 TB/s).
-// The bound is the weight stream; one-token calls of 17 MB are mostly a launch and two memory
-// latencies, and from 16 tokens on X, read again by every row block, costs more than W.
+// Measured (us, in a replayed graph; weights in the 256 MB last-level cache / from HBM): 1 x 4096 x
+// 4096 5.9 / 6.6 (2.5 TB/s), 8 x 4096 x 14336 13.5 / 15.6 (3.8 TB/s), 2:4 1 x 4096 x 14336 9.8 / 11.1
+// (3.3 TB/s), GLU 1 x 14336 x 4096 25.7 / 26.1 (4.5 TB/s).  The bound is the weight stream; one-token
+// calls of 17 MB are mostly a launch and two memory latencies, and from 16 tokens on X, read
+// again by every row block, costs more than W.
 #include "i8_device.h"
 
 namespace {

@@ -375,11 +375,15 @@ __device__ __forceinline__ void i8_finish(const i32x4 (&acc)[FI][FJ], const I8Ep
 
 // BM x BN: weight rows by tokens of a tile (GLU: BM / 2 outputs); WM x WN waves; NST stages.
 // Two stages of 256 x 256 (dense): bound by the matrix pipe under the card's power limit.  8192 x
-// 14336 x 4096 379-391 us, 2.5 POPS; the products alone on the same codes take 281 us (on constant
-// ones 238: the clock falls with the bits that change).  GLU 4096 x 14336 x 4096 383-395 us.
-// Rings of smaller tiles: bound by weights from HBM with few tokens (61 x 4096 x 14336 15.3 us with
-// its reduction, GLU 8 x 14336 x 4096 23-25 us, 4.9 TB/s), by the requests' latency in between
-// (2:4 333 x 4096 x 6144 16.8 us: 48 steps of 0.3 us).
+// 14336 x 4096 379-405 us on different cards, 2.4-2.5 POPS; the products alone on the same codes
+// take 281 us (on constant ones 238: the clock falls with the bits that change).  GLU 4096 x
+// 14336 x 4096 383-395 us.
+// Rings of smaller tiles (us; weights in the last-level cache / from HBM): with few tokens bound
+// by the weights' stream (61 x 4096 x 14336 15.4 / 21.9 with its reduction, 2:4 16 x 14336 x 4096
+// 8.9 / 11.6, 3.2 TB/s, GLU 8 x 14336 x 4096 24.4 / 27.1, 4.3 TB/s); in
+// between by the latency of a step's requests (2:4 333 x 4096 over 128 positions 4.9, over 6144
+// 17.2 / 23.5: 47 further steps of 0.26 / 0.40; dense 777 x 1025 over 16 4.7, over 1024 6.7, 2048
+// 8.1, 1999 9.4: rows 2000 bytes apart share cache lines with their neighbours).
 template <int BM, int BN, int WM, int WN, bool SP, bool GLU, int NST>
 __global__ __launch_bounds__(64 * WM * WN) void k_i8_tile(
     const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w0, const int8_t* __restrict__ w1, int64_t ldw,
@@ -1002,15 +1006,19 @@ struct MidPlan {
 // The largest tile that gives 192 workgroups (of 128 tokens only above 64); with none, the
 // smallest, a reduction of over 32 steps cut in ranges of at least 16 up to one workgroup per
 // CU.  A split costs the partial sums and a second kernel, 3-5 us against 0.13-0.15 us for each step
-// (100 x 500 x 2048 unsplit 5.0, in 8 ranges 7.7; x 8192 12.3 unsplit, 7.8 in 4, 8.4 in 8; 40 x
-// 256 x 14336 17.4 unsplit, 8.4 in 7, 9.3 in 14, 12.5 in 32), so it is the last choice, except
-// that 64 x 32 tiles pay for each step however little it holds: over 64 steps, 64 x 64 tiles in
-// two ranges.  Measured (us; 128 x 128 / 128 x 64 / 64 x 64 /
-// 64 x 32, split to fill the chip): dense 61 x 4096 x 14336 18.6 / 17.8 / 15.9 / 15.3, 777 x 1025 x
-// 1999 16.8 / 13.9 / 9.5 / 10.3, 128 x 4096 x 4096 17.8 / 13.5 / 11.0 / 8.5, 512 x 4096 x 4096
-// 19.1 / 13.4 / 15.6 / 20.1, 2048^3 13.1 / 15.9 / 17.4 / 21.4; 2:4 333 x 4096 x 6144 19.4 / 16.8 /
-// 19.6 / 20.6, 128 x 4096 x 14336 20.2 / 16.7 / 16.9 / 19.4, 1024 x 4096 x 4096 18.2 / 21.8 / 25.9 /
-// 33.2; GLU 64 x 14336 x 4096 26.4 / 25.5 / 29.1 / 33.7, 2:4 17.2 / 15.8 / 16.2 / 20.1.
+// of a short list of tiles (100 x 500 x 2048 unsplit 5.0, in 8 ranges 7.7; x 8192 12.3 unsplit, 7.8 in
+// 4, 8.4 in 8; 40 x 256 x 14336 17.4 unsplit, 8.4 in 7, 9.3 in 14, 12.5 in 32), so it is the last
+// choice, except that 64 x 32 tiles pay for each step however little it holds: over 64 steps, 64 x
+// 64 tiles in two ranges (weights from HBM, us, in two ranges / 64 x 32 unsplit: 128 x 4096 x 8320
+// 17.7 / 19.1, x 10240 21.1 / 23.8, x 14336 25.3 / 31.2, 100 x 4100 x 8320 19.9 / 19.8, x 14336 28.4 /
+// 31.6, 64 x 6400 x 8320 18.9 / 20.4, 2:4 128 x 4096 x 8320 16.7 / 17.6, x 14336 23.3 / 27.5, GLU 40 x
+// 4096 x 8320 18.8 / 20.0, x 14336 27.7 / 32.5).  Measured with weights in the last-level cache (us;
+// 128 x 128 / 128 x 64 / 64 x 64 / 64 x 32, split to fill the chip): dense 61 x 4096 x 14336 18.6 /
+// 17.8 / 15.9 / 15.3, 777 x 1025 x 1999 16.8 / 13.9 / 9.5 / 10.3, 128 x 4096 x 4096 17.8 / 13.5 / 11.0 /
+// 8.5, 512 x 4096 x 4096 19.1 / 13.4 / 15.6 / 20.1, 2048^3 13.1 / 15.9 / 17.4 / 21.4; 2:4 333 x 4096 x
+// 6144 19.4 / 16.8 / 19.6 / 20.6, 128 x 4096 x 14336 20.2 / 16.7 / 16.9 / 19.4, 1024 x 4096 x 4096
+// 18.2 / 21.8 / 25.9 / 33.2; GLU 64 x 14336 x 4096 26.4 / 25.5 / 29.1 / 33.7, 2:4 17.2 / 15.8 / 16.2 /
+// 20.1.
 MidPlan mid_plan(int64_t t, int64_t o, int64_t k, bool glu) {
   const int64_t steps = (k + 127) / 128;
   const int bm[4] = {128, 128, 64, 64}, bn[4] = {128, 64, 64, 32};

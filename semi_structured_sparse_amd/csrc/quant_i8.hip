@@ -19,7 +19,8 @@
 // with N != 4 passes the codes through LDS, where a window is four bytes at an even offset).
 // The kernel moves 2 + 1 (lifted 2 + 2(N-1)/N) bytes per value and is bound by memory: 8191 x
 // 4096 lifted for 6:8 (118 MB) 18.2 us, 6.5 TB/s (part of it from the last-level cache); with a
-// selection also by its network, 2048 x 14336 at 8:16 (88 MB) 21.8 us, 4.0 TB/s; one row 2.5 us.
+// selection also by its network, 2048 x 14336 at 8:16 (88 MB) 21.9 us, 4.0 TB/s; one row 2.5 us.
+// (In a replayed graph; under the profiler the selection takes 24.)
 #include "i8_device.h"
 
 namespace {
