@@ -196,13 +196,19 @@ def _ld(t, default=0):
 
 _current_raw_stream = None      # device -> raw current stream
 _current_device = None          # () -> the current device
-_half = None                    # torch.float16, which the int8 layers refuse where bf16 is meant
+# element types of the int8 layers: codes, rows of bf16 (or their bits), and fp16, which y must not be
+_int8s = _bf16s = _half = None
+
+
+def _bind_types(torch):
+    global _int8s, _bf16s, _half
+    _int8s, _bf16s, _half = (torch.int8, torch.uint8), (torch.bfloat16, torch.int16, torch.uint16), torch.float16
 
 
 def _bind_torch():
-    global _current_raw_stream, _current_device, _half
+    global _current_raw_stream, _current_device
     import torch
-    _half = torch.float16
+    _bind_types(torch)
     torch.cuda.current_stream()             # initialises the device
     raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
     # building a Stream object costs 2.7 us a call, the raw handle 0.2 us (one-token calls take 6)
@@ -510,13 +516,13 @@ def _refuse(t, dev, what):
     raise ValueError(what)
 
 
-def _mat(t, dev, size):
-    """(pointer, leading dimension) of a matrix with contiguous rows of `size`-byte elements."""
+def _mat(t, dev, types, name):
+    """(pointer, leading dimension) of a matrix with contiguous rows of one of the types."""
     if t is None or type(t) is int:
         return t, 0
     st = t.stride()
-    if len(st) != 2 or st[1] != 1 or t.get_device() != dev or t.element_size() != size:
-        _refuse(t, dev, f"a matrix with contiguous rows of {size}-byte elements is needed")
+    if len(st) != 2 or st[1] != 1 or t.get_device() != dev or t.dtype not in types:
+        _refuse(t, dev, f"a matrix with contiguous rows of {name} is needed")
     return t.data_ptr(), st[0]
 
 
@@ -538,8 +544,8 @@ def _codes(m, sh, dev, rows, cols, ld):
     if sh is None:
         return m, ld or 0
     st = m.stride()
-    if len(st) != 2 or st[1] != 1 or m.get_device() != dev or m.element_size() != 1:
-        _refuse(m, dev, "a matrix with contiguous rows of 1-byte elements is needed")
+    if len(st) != 2 or st[1] != 1 or m.get_device() != dev or m.dtype not in _int8s:
+        _refuse(m, dev, "a matrix with contiguous rows of int8 codes is needed")
     if ld is None:
         ld = st[0] if cols else 0       # of no columns: torch has 1
     if sh[0] < rows or sh[1] < cols + -cols % 16 or ld != st[0]:
@@ -602,8 +608,8 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
         dev, stream = _current()
     else:
         dev, stream = _device_of(x, q, scale), _stream(stream)
-    xp, lx = _mat(x, dev, 2)
-    qp, lq = _mat(q, dev, 1)
+    xp, lx = _mat(x, dev, _bf16s, "bf16 values")
+    qp, lq = _mat(q, dev, _int8s, "int8 codes")
     if ldx is not None:
         lx = ldx
     if ldq is not None:
@@ -614,8 +620,6 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
             rows = have
         if k is None:
             k = width
-        if x.dtype is _half:
-            raise ValueError("x of bf16 values is needed")
         if width < k:
             raise ValueError(f"x of rows of {k} values is needed")
         if have < rows or width & 7 or ldx is not None:

@@ -25,7 +25,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(S, "lib", lambda: rec)
     monkeypatch.setattr(S, "_current_device", lambda: -1)
     monkeypatch.setattr(S, "_current_raw_stream", lambda dev: 0)
-    monkeypatch.setattr(S, "_half", torch.float16)
+    S._bind_types(torch)
     return rec.calls
 
 
@@ -234,3 +234,24 @@ def test_rows_of_no_values_are_valid():
     """The library itself (nothing to launch: no rows)."""
     assert S.lib().nm_quant_i8(None, 0, 0, 0, 0, 0, 2, None, 0, None, None) == S.NM_OK
     assert S.lib().nm_quant_i8(None, 0, 0, 1, 0, 0, 2, None, 0, None, None) == S.NM_EALIGN
+
+
+# --------------------------------------------------------------------------- element types ---
+
+def test_one_byte_floats_are_no_codes(calls):
+    """fp8 weights and activations are other operators' operands: their bytes are not integers."""
+    x, q, s, y = bf16(4, 64), i8(4, 64), torch.zeros(64), torch.zeros(4, 8)
+    w = i8(8, 64)
+    for dt in (torch.float8_e4m3fn, torch.float8_e5m2, torch.bool):
+        refused(calls, S.nm_quant_i8, x, q.to(dt), s)
+        for call in (product, gated):
+            refused(calls, call, q.to(dt), w, y)
+            refused(calls, call, q, w.to(dt), y)
+        refused(calls, gated, q, w, y, up=w.to(dt))
+    refused(calls, S.nm_quant_i8, x.half(), q, s)
+    for dt in (torch.int8, torch.uint8):                                    # the codes' bits
+        taken(calls, S.nm_quant_i8, x, q.to(dt), s)
+        for call in (product, gated):
+            taken(calls, call, q.to(dt), w.to(dt), y)
+    for dt in (torch.int16, torch.uint16):                                  # bf16 bits
+        taken(calls, S.nm_quant_i8, x.view(dt), q, s)
