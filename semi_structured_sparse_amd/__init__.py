@@ -212,11 +212,13 @@ def _bind_torch():
     torch.cuda.current_stream()             # initialises the device
     raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
     # building a Stream object costs 2.7 us a call, the raw handle 0.2 us (one-token calls take 6)
+    # the stream lookup last: it tells other threads that all of it is there
     if raw is not None and device is not None:
-        _current_raw_stream, _current_device = raw, device
+        _current_device = device
+        _current_raw_stream = raw
     else:
-        _current_raw_stream = lambda dev: torch.cuda.current_stream(dev).cuda_stream  # noqa: E731
         _current_device = torch.cuda.current_device
+        _current_raw_stream = lambda dev: torch.cuda.current_stream(dev).cuda_stream  # noqa: E731
 
 
 def _current():
@@ -633,8 +635,7 @@ def nm_quant_i8(x, q, scale, n=0, m=0, ns=2, stream=None, *, rows=None, k=None, 
             _holds(q, rows, kq, 16, lq)
     if k == 0:                           # torch has a leading dimension of 1 for no columns
         lx, lq = ldx or 0, ldq or 0
-    st = lib().nm_quant_i8(xp, rows, k, lx, n, m, ns, qp, lq, _factors(scale, rows, dev),
-                           stream)
+    st = lib().nm_quant_i8(xp, rows, k, lx, n, m, ns, qp, lq, _factors(scale, rows, dev), stream)
     if check and st:
         _check(st, "nm_quant_i8")
     return st
@@ -699,8 +700,8 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
     if stream is None:
         dev, stream = _current()
     else:
-        dev, stream = _device_of(x, w_gate, y, w_up, x_scale, gate_scale, up_scale, gate_meta,
-                                up_meta, workspace), _stream(stream)
+        dev, stream = _device_of(x, w_gate, y, w_up, x_scale, gate_scale, up_scale, gate_meta, up_meta,
+                                 workspace), _stream(stream)
     sx = None if x is None or type(x) is int else x.shape
     sg = None if w_gate is None or type(w_gate) is int else w_gate.shape
     su = None if w_up is None or type(w_up) is int else w_up.shape

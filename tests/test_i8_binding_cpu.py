@@ -2,6 +2,8 @@
 replaced by a recorder and the tensors live on the CPU (the binding takes -1, their device, for
 the current one).  A call whose memory the tensors do not hold must be refused before the
 library is reached; the calls that the layouts allow must reach it with the right arguments."""
+import sys
+
 import pytest
 
 import semi_structured_sparse_amd as S
@@ -255,3 +257,33 @@ def test_one_byte_floats_are_no_codes(calls):
             taken(calls, call, q.to(dt), w.to(dt), y)
     for dt in (torch.int16, torch.uint16):                                  # bf16 bits
         taken(calls, S.nm_quant_i8, x.view(dt), q, s)
+
+
+# ----------------------------------------------------------------------------- first calls ---
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_first_calls_of_two_threads(monkeypatch, raw):
+    """At no point of the first call's binding may another thread find part of it: the stream
+    lookup, which tells that the rest is there, comes last."""
+    for name in ("_current_raw_stream", "_current_device", "_int8s", "_bf16s", "_half"):
+        monkeypatch.setattr(S, name, None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: None)
+    if raw:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    seen = []
+
+    def step(frame, event, arg):
+        frame.f_trace_opcodes = True
+        seen.append(S._current_raw_stream is None or None not in (S._current_device, S._int8s, S._bf16s, S._half))
+        return step
+
+    before = sys.gettrace()
+    sys.settrace(step)
+    try:
+        S._bind_torch()
+    finally:
+        sys.settrace(before)
+    assert len(seen) > 20 and all(seen) and S._current_raw_stream is not None
