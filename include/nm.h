@@ -650,6 +650,64 @@ nm_status nm_glu_i8(const int8_t* x, int64_t t, int64_t k, int64_t ldx, const fl
 /* Workspace bytes of the preferred route of nm_spmm_i8 (glu = 0) or nm_glu_i8 (glu = 1). */
 int64_t nm_i8_workspace_size(int64_t t, int64_t o, int64_t k, int sparse, int glu, uint32_t route);
 
+/*
+ * ------------------------------------------------------------------------------------
+ * What stands around the products in a decoder layer: the norm that writes their operands, the
+ * routing of tokens to experts.
+ */
+
+/*
+ * nm_rmsnorm_i8 -- root-mean-square norm of rows with the residual's addition, written as int8
+ * codes with one scale per row (the operands of nm_spmm_i8 and nm_glu_i8), after a selection
+ * ([FLEX] 2.A) or lifted for (2N-2):2N weights ([SLIDE] 2.B).  Per row:
+ *   s = x + residual, one fp32 sum rounded to the stream's type (s = x without a residual)
+ *   p[k] = fp32(s[k] weight[k]),   rstd = 1 / sqrt(sum_k s[k]^2 / k + eps), in fp64
+ *   q[k] = 127 p[k] / max|p|, the exact quotient rounded to the nearest integer, ties to even;
+ *          with a pattern (m > 0) 0 where p[k] is not among the n largest |p| of its group of m,
+ *          ties to the lower index;   scale = fp32(max|p| rstd / 127)
+ *   y[k] = bf16(fp32(p[k] fp32(rstd))), unselected
+ * so q[k] scale is the normed row in 8 bits.  A row of zeros gets zero codes and the scale 1; a
+ * row whose p holds an infinity or a NaN that as its scale and zero codes (its y is what the
+ * formula gives).  Codes, sum_out are bit-exact.
+ *   x         x_dtype [rows][ldx];  residual, sum_out: stream_dtype [rows][ldr], [rows][lds], or
+ *             NULL; sum_out receives s and needs a residual (NM_EINVAL); it may be the residual,
+ *             or x where their types agree, with the same leading dimension, and overlap neither
+ *             otherwise
+ *   weight    fp32 [k], or NULL for ones;  eps > 0, finite
+ *   y         bf16 [rows][ldy] or NULL (a router's or a bf16 product's operand)
+ *   n, m, ns, q, ldq, scale   as for nm_quant_i8
+ * Every leading dimension is a multiple of 8 elements (ldq of 16); rows of x and residual are
+ * read up to a multiple of 8 elements, and nothing past k of sum_out and y is written.
+ * k <= 32768 (NM_EUNSUPPORTED above).  y, q and scale must not overlap another argument.
+ */
+nm_status nm_rmsnorm_i8(const void* x, nm_ydtype x_dtype, int64_t rows, int64_t k, int64_t ldx, const void* residual,
+                        int64_t ldr, void* sum_out, int64_t lds, nm_ydtype stream_dtype, const float* weight, float eps,
+                        int n, int m, int ns, void* y, int64_t ldy, int8_t* q, int64_t ldq, float* scale, void* stream);
+
+#define NM_MOE_MAX_EXPERTS 1024
+#define NM_MOE_MAX_TOP 32
+
+typedef enum { NM_ROUTER_SOFTMAX = 0, NM_ROUTER_SIGMOID = 1 } nm_router;
+
+/*
+ * nm_moe_route -- the experts of each token and their weights, from the router's logits (an fp32
+ * product, nm_linear or nm_spmm).  Of the experts whose logit is neither -inf nor NaN the `top`
+ * with the largest score are chosen, the largest first, ties to the lower index.
+ *   NM_ROUTER_SOFTMAX  score = logit;  weight = e^logit / sum over all experts e^logit
+ *   NM_ROUTER_SIGMOID  score = weight = 1 / (1 + e^-logit); with a bias score = that + bias[e] in
+ *                      fp64, for the choice alone
+ * then, with renormalize = 1, weights are divided by the sum of the chosen ones, and multiplied
+ * by `scale`.  A slot that no expert is left for gets the id -1 and the weight 0 (all slots of a
+ * row whose logits are all -inf); weights whose sum is 0 are 0.
+ *   logits   fp32 [t][ldl], ldl >= experts;  bias fp32 [experts], finite, or NULL; with softmax:
+ *            NM_EUNSUPPORTED
+ *   ids      int32 [t][top];  weights fp32 [t][top]
+ * 1 <= top <= experts (NM_EINVAL, NM_ESHAPE); experts <= NM_MOE_MAX_EXPERTS, top <=
+ * NM_MOE_MAX_TOP, t <= 2^25 (NM_EUNSUPPORTED above).
+ */
+nm_status nm_moe_route(const float* logits, int64_t t, int64_t experts, int64_t ldl, const float* bias, nm_router kind,
+                       int top, int renormalize, float scale, int32_t* ids, float* weights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

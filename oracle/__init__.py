@@ -834,3 +834,82 @@ def glu_gate(g: np.ndarray, act: str) -> np.ndarray:
     z = g if act == "silu" else 2.0 * np.sqrt(2.0 / np.pi) * (g + 0.044715 * g ** 3)
     with np.errstate(over="ignore"):
         return g / (1.0 + np.exp(-z))
+
+
+# --------------------------------------------------- operators around the products, fp64
+# The norm that writes int8 codes, and the routing of tokens to experts.
+
+def bf16_round(v: np.ndarray) -> np.ndarray:
+    """fp32 values -> the nearest bf16 values, as fp32 (ties to even; finite and infinite)."""
+    return f32_from_bf16(bf16_from_f32_rne(v))
+
+
+def keep_largest(p: np.ndarray, n: int, m: int) -> np.ndarray:
+    """bool [R][K]: the n largest |p| of each group of m, ties to the lower index."""
+    rows, k = p.shape
+    g = np.abs(p).reshape(rows, k // m, m)
+    order = np.argsort(-g, axis=2, kind="stable")[:, :, :n]
+    keep = np.zeros(g.shape, bool)
+    np.put_along_axis(keep, order, True, axis=2)
+    return keep.reshape(rows, k)
+
+
+def rmsnorm_i8(x: np.ndarray, residual=None, stream: str = "bf16", weight=None, eps: float = 1e-6, n: int = 0,
+               m: int = 0, ns: int = 2):
+    """fp32 values x [R][K] (+ residual) -> (codes int8 [R][K or K'], scale fp64 [R], s fp32 [R][K],
+    y fp64 [R][K]).  s = x + residual rounded to the stream's type, p = fp32(s weight), codes =
+    127 p / max|p| to the nearest integer, ties to even: the quotient in fp64, where a tie of
+    24-bit values is exact and everything else stays on its side (2^-25 of a unit at least).
+    scale = max|p| / (127 rms), y = p / rms, rms = sqrt(mean s^2 + eps).  Zero rows: scale 1; rows
+    with an infinity or a NaN in p: that as scale, zero codes."""
+    s = np.asarray(x, np.float32)
+    if residual is not None:
+        with np.errstate(over="ignore", invalid="ignore"):
+            s = s + np.asarray(residual, np.float32)
+        if stream == "bf16":
+            s = bf16_round(s)
+    rows, k = s.shape
+    with np.errstate(invalid="ignore", over="ignore"):
+        p = s if weight is None else s * np.asarray(weight, np.float32)[None, :]
+        s64, p64 = s.astype(np.float64), p.astype(np.float64)
+        rms = np.sqrt((s64 ** 2).sum(1) / max(k, 1) + np.float64(np.float32(eps)))
+        amax = np.abs(p64).max(axis=1) if k else np.zeros(rows)
+        bad = ~np.isfinite(amax)
+        usable = ~bad & (amax > 0)
+        safe = np.where(usable, amax, 1.0)
+        codes = np.rint(127.0 * np.where(usable[:, None], p64, 0.0) / safe[:, None]).astype(np.int8)
+        scale = np.where(bad, amax, np.where(usable, safe / (127.0 * rms), 1.0))
+        y = p64 / rms[:, None]
+    if m:
+        codes = np.where(keep_largest(np.where(usable[:, None], p64, 0.0), n, m), codes, np.int8(0))
+    if ns > 2:
+        codes = lift(codes.astype(np.int8).view(np.uint8).astype(np.uint16), ns).astype(np.uint8).view(np.int8)
+    return codes, scale, s, y
+
+
+def moe_route(logits: np.ndarray, top: int, sigmoid: bool = False, bias=None, renormalize: bool = True,
+              scale: float = 1.0):
+    """fp32 logits [T][E] -> (ids int32 [T][top], weights fp64 [T][top]): one expert after another, the
+    largest score left, the lowest index of equals, none whose logit is -inf or NaN (id -1, weight
+    0)."""
+    t, e = logits.shape
+    ids = np.full((t, top), -1, np.int32)
+    weights = np.zeros((t, top))
+    for r in range(t):
+        v = [float(a) for a in logits[r]]
+        with np.errstate(over="ignore"):
+            sig = [1.0 / (1.0 + np.exp(-np.float64(a))) if a > -np.inf else 0.0 for a in v]
+        score = v if bias is None else [sig[i] + float(bias[i]) for i in range(e)]
+        left = [i for i in range(e) if v[i] > -np.inf]
+        mx = max((v[i] for i in left), default=0.0)
+        soft = {i: 1.0 if v[i] == mx else float(np.exp(v[i] - mx)) for i in left}
+        total = sum(soft.values())
+        for j in range(min(top, len(left))):
+            best = max(left, key=lambda i: (score[i], -i))
+            left.remove(best)
+            ids[r, j] = best
+            weights[r, j] = sig[best] if sigmoid else soft[best] / total
+        whole = weights[r].sum()
+        if renormalize:
+            weights[r] = weights[r] / whole if whole > 0 else 0.0
+    return ids, weights * float(np.float32(scale))

@@ -27,6 +27,7 @@ __all__ = [
     "NM_PTS_STATIC", "NM_PTS_VAR", "nm_sparsify_pts", "nm_weight_sums", "NM_ESCRATCH", "nm_spmm_noalloc",
     "NM_NOALLOC_SCRATCH_BYTES", "nm_quant_i8", "nm_meta_block", "nm_meta_block_bytes", "nm_spmm_i8", "nm_glu_i8",
     "nm_i8_workspace_size", "NM_I8_MAX_K", "NM_I8_MAX_ROWS", "NM_Y_F32", "NM_Y_BF16", "NM_GLU_SILU", "NM_GLU_GELU_TANH",
+    "nm_rmsnorm_i8", "nm_moe_route", "NM_MOE_MAX_EXPERTS", "NM_MOE_MAX_TOP", "NM_ROUTER_SOFTMAX", "NM_ROUTER_SIGMOID",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnmsparse.so")
@@ -43,6 +44,8 @@ NM_I8_MAX_K = 131071
 NM_I8_MAX_ROWS = 1 << 27
 NM_Y_F32, NM_Y_BF16 = 0, 1
 NM_GLU_SILU, NM_GLU_GELU_TANH = 0, 1
+NM_MOE_MAX_EXPERTS, NM_MOE_MAX_TOP = 1024, 32
+NM_ROUTER_SOFTMAX, NM_ROUTER_SIGMOID = 0, 1
 
 # route hints (NM_ROUTE_*) and the report of what ran (NM_TAKEN_*), by lower-case name
 ROUTE = {name: 1 << i for i, name in enumerate(
@@ -169,6 +172,11 @@ def lib() -> ctypes.CDLL:
                             _int, _vp, _i64, ctypes.c_uint32, _vp, _vp]
     L.nm_i8_workspace_size.restype = _i64
     L.nm_i8_workspace_size.argtypes = [_i64, _i64, _i64, _int, _int, ctypes.c_uint32]
+    L.nm_rmsnorm_i8.restype = _int
+    L.nm_rmsnorm_i8.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, ctypes.c_float, _int, _int,
+                                _int, _vp, _i64, _vp, _i64, _vp, _vp]
+    L.nm_moe_route.restype = _int
+    L.nm_moe_route.argtypes = [_vp, _i64, _i64, _i64, _vp, _int, _int, _int, ctypes.c_float, _vp, _vp, _vp]
     _LIB = L
     return L
 
@@ -198,11 +206,13 @@ _current_raw_stream = None      # device -> raw current stream
 _current_device = None          # () -> the current device
 # element types of the int8 layers: codes, rows of bf16 (or their bits), and fp16, which y must not be
 _int8s = _bf16s = _half = None
+_f32s = _int32s = None          # of the operators around the products
 
 
 def _bind_types(torch):
-    global _int8s, _bf16s, _half
+    global _int8s, _bf16s, _half, _f32s, _int32s
     _int8s, _bf16s, _half = (torch.int8, torch.uint8), (torch.bfloat16, torch.int16, torch.uint16), torch.float16
+    _f32s, _int32s = (torch.float32,), (torch.int32,)
 
 
 def _bind_torch():
@@ -728,3 +738,93 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
     if check and st:
         _check(st, "nm_glu_i8")
     return st
+
+
+# ------------------------------------------------------ operators around the products ---
+
+def _rows_of(t, dev, rows, cols, whole, ld, kind, name):
+    """(pointer, leading dimension, NM_Y_*) of `rows` rows of `cols` fp32 or bf16 values, read or
+    written in pieces of `whole`; ld: None, or a leading dimension in place of the tensor's; kind: the
+    type of raw pointers (None: fp32), which a tensor has to agree with."""
+    if t is None or type(t) is int:
+        return t, ld or 0, NM_Y_F32 if kind is None else kind
+    st = t.stride()
+    have = NM_Y_F32 if t.dtype in _f32s else NM_Y_BF16 if t.dtype in _bf16s else -1
+    if len(st) != 2 or st[1] != 1 or t.get_device() != dev or have < 0 or (kind is not None and kind != have):
+        _refuse(t, dev, f"{name}: a matrix with contiguous rows of fp32 or bf16 values is needed")
+    sh = t.shape
+    if ld is None:
+        ld = st[0] if cols else 0       # of no columns: torch has 1
+    if sh[0] < rows or sh[1] < cols + -cols % whole or ld != st[0]:
+        _holds(t, rows, cols, whole, ld)
+    return t.data_ptr(), ld, have
+
+
+def _list_of(t, n, dev, types, name):
+    """Pointer of at least n contiguous values of one of the types (None -> NULL, integers are raw
+    pointers)."""
+    if t is None or type(t) is int:
+        return t
+    if t.get_device() != dev or t.dtype not in types or t.numel() < n or not t.is_contiguous():
+        _refuse(t, dev, f"{name}: {n} contiguous values are needed")
+    return t.data_ptr()
+
+
+def nm_rmsnorm_i8(x, weight, q, scale, residual=None, sum_out=None, y=None, eps=1e-6, n=0, m=0, ns=2, stream=None, *,
+                  rows=None, k=None, ldx=None, ldr=None, lds=None, ldy=None, ldq=None, x_dtype=None, stream_dtype=None,
+                  check=True):
+    """RMS norm of x (+ residual, the sum to sum_out) as int8 codes q with one fp32 scale per row, and
+    in bf16 to y if given (include/nm.h)."""
+    if stream is None:
+        dev, stream = _current()
+    else:
+        dev, stream = _device_of(x, q, scale, weight, residual, sum_out, y), _stream(stream)
+    if rows is None:
+        rows = x.shape[0]
+    if k is None:
+        k = x.shape[1]
+    xp, lx, xt = _rows_of(x, dev, rows, k, 8, ldx, x_dtype, "x")
+    rp, lr, rt = _rows_of(residual, dev, rows, k, 8, ldr, stream_dtype, "residual")
+    sp, ls, st = _rows_of(sum_out, dev, rows, k, 1, lds, rt if residual is not None else stream_dtype, "sum_out")
+    yp, ly, _ = _rows_of(y, dev, rows, k, 1, ldy, NM_Y_BF16, "y")
+    qp, lq = _mat(q, dev, _int8s, "int8 codes")
+    if ldq is not None:
+        lq = ldq
+    if qp is not q:
+        kq = k // (2 * ns) * 4 * (ns - 1) if ns > 2 else k
+        have, width = q.shape
+        if width < kq:
+            raise ValueError(f"q of rows of {kq} codes is needed")
+        if have < rows or width & 15 or ldq is not None:
+            _holds(q, rows, kq, 16, lq)
+    if k == 0:
+        lq = ldq or 0
+    res = lib().nm_rmsnorm_i8(xp, xt, rows, k, lx, rp, lr, sp, ls, rt if residual is not None else st,
+                              _list_of(weight, k, dev, _f32s, "weight"), eps, n, m, ns, yp, ly, qp, lq,
+                              _list_of(scale, rows, dev, _f32s, "scale"), stream)
+    if check and res:
+        _check(res, "nm_rmsnorm_i8")
+    return res
+
+
+def nm_moe_route(logits, ids, weights, kind=NM_ROUTER_SOFTMAX, bias=None, renormalize=True, scale=1.0, stream=None, *,
+                 t=None, experts=None, top=None, ldl=None, check=True):
+    """The experts of each token (ids, int32 [t][top], -1 where none is left) and their fp32 weights from
+    fp32 logits [t][experts] (include/nm.h)."""
+    if stream is None:
+        dev, stream = _current()
+    else:
+        dev, stream = _device_of(logits, ids, weights, bias), _stream(stream)
+    if t is None:
+        t = logits.shape[0]
+    if experts is None:
+        experts = logits.shape[1]
+    if top is None:
+        top = ids.shape[1]
+    lp, ll, _ = _rows_of(logits, dev, t, experts, 1, ldl, NM_Y_F32, "logits")
+    res = lib().nm_moe_route(lp, t, experts, ll, _list_of(bias, experts, dev, _f32s, "bias"), kind, top,
+                             1 if renormalize else 0, scale, _list_of(ids, t * top, dev, _int32s, "ids"),
+                             _list_of(weights, t * top, dev, _f32s, "weights"), stream)
+    if check and res:
+        _check(res, "nm_moe_route")
+    return res

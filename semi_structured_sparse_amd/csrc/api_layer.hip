@@ -1,0 +1,73 @@
+// C ABI of the operators around the products: host-side validation and dispatch
+// (nm_rmsnorm_i8, nm_moe_route).  Arguments are checked completely before the first HIP call.
+#include "layer_launch.h"
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <typename... P>
+bool all_aligned(P... p) { return (aligned16(p) && ...); }
+
+// rows x ld elements of up to 8 bytes addressable in 64 bits
+bool span_ok(int64_t rows, int64_t ld) {
+  int64_t e, b;
+  return rows >= 0 && ld >= 0 && !__builtin_mul_overflow(rows, ld, &e) && !__builtin_mul_overflow(e, (int64_t)8, &b);
+}
+
+bool is_dtype(int d) { return d == NM_Y_F32 || d == NM_Y_BF16; }
+
+bool finite(float v) { return v - v == 0.0f; }
+
+nm_status hip_status(hipError_t e) { return e == hipSuccess ? NM_OK : NM_EHIP; }
+
+int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
+
+}  // namespace
+
+extern "C" {
+
+nm_status nm_rmsnorm_i8(const void* x, nm_ydtype x_dtype, int64_t rows, int64_t k, int64_t ldx, const void* residual,
+                        int64_t ldr, void* sum_out, int64_t lds, nm_ydtype stream_dtype, const float* weight, float eps,
+                        int n, int m, int ns, void* y, int64_t ldy, int8_t* q, int64_t ldq, float* scale, void* stream) {
+  if (m != 0 && m != 4 && m != 8 && m != 16 && m != 32) return m < 0 ? NM_EINVAL : NM_EUNSUPPORTED;
+  if (m != 0 && (n < 1 || n > m)) return NM_EINVAL;
+  if (ns < 2 || ns > 8) return NM_EINVAL;
+  if (!is_dtype(x_dtype) || !is_dtype(stream_dtype)) return NM_EINVAL;
+  if (!(eps > 0.0f) || !finite(eps)) return NM_EINVAL;
+  if (sum_out != nullptr && residual == nullptr) return NM_EINVAL;
+  if (m != 0 && ns != 2) return NM_EUNSUPPORTED;
+  if (rows < 0 || k < 0) return NM_ESHAPE;
+  if (m != 0 && k % m != 0) return NM_ESHAPE;
+  if (ns > 2 && k % (2 * ns) != 0) return NM_ESHAPE;
+  if (rows > 0 && (scale == nullptr || (k > 0 && (x == nullptr || q == nullptr)))) return NM_EINVAL;
+  const int64_t kq = ns > 2 ? k / (2 * ns) * 4 * (ns - 1) : k;
+  const bool has_r = residual != nullptr, has_s = sum_out != nullptr, has_y = y != nullptr;
+  if (ldx < k || ldq < up16(kq) || (has_r && ldr < k) || (has_s && lds < k) || (has_y && ldy < k)) return NM_ESHAPE;
+  if (!span_ok(rows, ldx) || !span_ok(rows, ldq) || (has_r && !span_ok(rows, ldr)) || (has_s && !span_ok(rows, lds)) ||
+      (has_y && !span_ok(rows, ldy)))
+    return NM_ESHAPE;
+  if (!all_aligned(x, residual, sum_out, weight, y, q, scale)) return NM_EALIGN;
+  if (ldx % 8 != 0 || ldq % 16 != 0 || (has_r && ldr % 8 != 0) || (has_s && lds % 8 != 0) || (has_y && ldy % 8 != 0))
+    return NM_EALIGN;
+  if (k > 32768 || rows > 0x7FFFFFFF) return NM_EUNSUPPORTED;
+  const nml::NormArgs a{x, residual, sum_out, weight, static_cast<uint16_t*>(y), q, scale, rows, k, ldx, ldr, lds, ldy,
+                        ldq, x_dtype == NM_Y_BF16, stream_dtype == NM_Y_BF16, eps, n, m, ns};
+  return hip_status(nml::launch_rmsnorm_i8(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+nm_status nm_moe_route(const float* logits, int64_t t, int64_t experts, int64_t ldl, const float* bias, nm_router kind,
+                       int top, int renormalize, float scale, int32_t* ids, float* weights, void* stream) {
+  if (kind != NM_ROUTER_SOFTMAX && kind != NM_ROUTER_SIGMOID) return NM_EINVAL;
+  if (renormalize != 0 && renormalize != 1) return NM_EINVAL;
+  if (!finite(scale) || top < 1) return NM_EINVAL;
+  if (t < 0 || experts < top || ldl < experts || !span_ok(t, ldl)) return NM_ESHAPE;
+  if (t > 0 && (logits == nullptr || ids == nullptr || weights == nullptr)) return NM_EINVAL;
+  if (!all_aligned(logits, bias, ids, weights)) return NM_EALIGN;
+  if (bias != nullptr && kind != NM_ROUTER_SIGMOID) return NM_EUNSUPPORTED;
+  if (experts > NM_MOE_MAX_EXPERTS || top > NM_MOE_MAX_TOP || t > (1 << 25)) return NM_EUNSUPPORTED;
+  const nml::RouteArgs a{logits, bias, ids, weights, t, experts, ldl, top, kind == NM_ROUTER_SIGMOID, renormalize, scale};
+  return hip_status(nml::launch_moe_route(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

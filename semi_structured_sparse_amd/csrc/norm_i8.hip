@@ -1,0 +1,400 @@
+// RMS norm of rows with the residual's addition, written as int8 codes with one scale per row,
+// after an n:m selection or lifted for (2N-2):2N weights (SlideSparse page, technical summary 2.B;
+// Flexible (N:M) Activation Sparsity page, 2.A).
+//
+//   s = x + r, rounded to the stream's type     p = fp32(s w)
+//   rstd = 1 / sqrt(sum s^2 / k + eps)          y = bf16(p fp32(rstd))
+//   q = the integer nearest to 127 p / max|p|   scale = max|p| rstd / 127
+//
+// The row's factor rstd multiplies value and maximum alike, so the codes do not hang on it, nor
+// on the order of the sum: they are those of p, and exact.  p has 24 bits, where one fp32
+// quotient may fall on the wrong side of a half: t = p fp32(127 / max) is off by at most 127 *
+// 2^-23 = 1.52e-5 (the quotient and the product round once each), so a code whose t lies more
+// than 2e-5 from a half is right, and the others, one in 25000, are divided again in fp64.
+// There 127 p is exact, and since p and max are 24-bit integers times powers of two, a quotient
+// that is no half differs from one by at least 2^-25 of a unit: far more than fp64 rounds.
+// The sum of squares is carried in fp64, so that no row overflows it.
+//
+// One pass: a row's p stay in registers between the reductions (the largest |p| and the sum
+// cross the workgroup together) and the outputs.  Bound by memory.
+#include "i8_device.h"
+#include "layer_launch.h"
+
+namespace {
+
+using namespace nmk;
+using namespace nml;
+
+struct RowCode {
+  float f, r;        // t = (p f) r: f a power of two that keeps r finite, r = 127 / (max f)
+  float amax;
+  bool zero;         // every code is 0
+};
+
+__device__ __forceinline__ RowCode row_code(uint32_t mk) {
+  RowCode c;
+  c.amax = __uint_as_float(mk);
+  c.zero = mk == 0 || mk >= 0x7F800000u;
+  c.f = c.amax < 0x1p-40f ? 0x1p90f : 1.0f;
+  c.r = c.zero ? 0.0f : 127.0f / (c.amax * c.f);
+  return c;
+}
+
+// bits whose low byte is the code of p
+__device__ __forceinline__ uint32_t code_of(float p, const RowCode& c) {
+  const float t = (p * c.f) * c.r;
+  const float u = t + 12582912.0f;               // 1.5 * 2^23: the nearest integer, ties to even
+  const float d = t - (u - 12582912.0f);
+  uint32_t b = __float_as_uint(u);
+  if (__builtin_expect(__builtin_fabsf(d) > 0.49998f, 0)) b = (uint32_t)(int)__builtin_rint(127.0 * (double)p / (double)c.amax);
+  return b;
+}
+
+__device__ __forceinline__ uint32_t codes4(const float* p, const RowCode& c) {
+  const uint32_t c0 = code_of(p[0], c), c1 = code_of(p[1], c), c2 = code_of(p[2], c), c3 = code_of(p[3], c);
+  return __builtin_amdgcn_perm(c1, c0, 0x0C0C0400u) | __builtin_amdgcn_perm(c3, c2, 0x04000C0Cu);
+}
+
+// Keep bits of the n largest magnitudes of a group, ties to the lower index: the n-th largest
+// key, every key above it, and of the equal ones the first.
+template <int M, int NT>
+__device__ __forceinline__ uint32_t keep_bits(const float* p, int n) {
+  uint32_t k[M], s[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) s[i] = k[i] = __float_as_uint(p[i]) & 0x7FFFFFFFu;
+  sort_desc_oem<M>(s);
+  uint32_t tau = s[NT > 0 ? NT - 1 : 0];
+  if constexpr (NT > 0) {
+    n = NT;
+  } else {
+#pragma unroll
+    for (int j = 1; j < M; ++j) tau = j == n - 1 ? s[j] : tau;
+  }
+  int left = n;
+#pragma unroll
+  for (int i = 0; i < M; ++i) left -= k[i] > tau ? 1 : 0;
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const bool eq = k[i] == tau;
+    bits |= (k[i] > tau || (eq && left > 0) ? 1u : 0u) << i;
+    left -= eq ? 1 : 0;
+  }
+  return bits;
+}
+
+__device__ __forceinline__ void widen(const uint4& d, float* v) {
+  const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(e[j] << 16);
+    v[2 * j + 1] = __uint_as_float(e[j] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ void as_floats(const uint4& a, const uint4& b, float* v) {
+  const uint32_t e[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(e[j]);
+}
+
+// two fp32 values as packed bf16, to nearest even
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
+__device__ __forceinline__ uint4 narrow(const float* v) {
+  uint32_t e[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) e[j] = bf16x2(v[2 * j], v[2 * j + 1]);
+  return make_uint4(e[0], e[1], e[2], e[3]);
+}
+
+// UN units of PU pieces of 8 values a thread, the workgroup as many waves as the row needs.
+// WAVE: a row per wave, four rows a workgroup.  SEL: 0 none, M the group width (NK > 0: n known
+// at compile time).  LIFT: 0 none, 4 the N = 4 lift from registers, 1 any N through LDS.
+template <bool WAVE, int UN, int SEL, int NK, int LIFT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_rmsnorm_i8(NormArgs a) {
+  constexpr int PU = SEL > 8 ? SEL / 8 : 1, P = UN * PU;
+  __shared__ uint32_t red_max[WAVE ? 1 : 16];
+  __shared__ double red_sum[WAVE ? 1 : 16];
+  extern __shared__ __align__(16) unsigned char codes[];   // LIFT == 1: the rows' codes
+  const int NT = WAVE ? 64 : (int)blockDim.x;              // threads of a row
+  const int tid = WAVE ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (WAVE && row >= a.rows) return;   // whole waves; no barrier below for these
+  const int k = (int)a.k;
+  auto at = [&](int i) { return ((i / PU * NT + tid) * PU + i % PU) * 8; };   // first value of piece i
+
+  // every load of the row first: rows are readable in whole pieces (leading dimensions % 8 == 0)
+  uint4 xa[P], xb[P], ra[P], rb[P];
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < P; ++i) xa[i] = xb[i] = ra[i] = rb[i] = zero;
+  if (a.x_bf16) {
+    const uint16_t* xr = static_cast<const uint16_t*>(a.x) + row * a.ldx;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (at(i) < k) xa[i] = *reinterpret_cast<const uint4*>(xr + at(i));
+  } else {
+    const float* xr = static_cast<const float*>(a.x) + row * a.ldx;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (at(i) < k) {
+        xa[i] = *reinterpret_cast<const uint4*>(xr + at(i));
+        xb[i] = *reinterpret_cast<const uint4*>(xr + at(i) + 4);
+      }
+  }
+  if (a.r != nullptr) {
+    if (a.r_bf16) {
+      const uint16_t* rr = static_cast<const uint16_t*>(a.r) + row * a.ldr;
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (at(i) < k) ra[i] = *reinterpret_cast<const uint4*>(rr + at(i));
+    } else {
+      const float* rr = static_cast<const float*>(a.r) + row * a.ldr;
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (at(i) < k) {
+          ra[i] = *reinterpret_cast<const uint4*>(rr + at(i));
+          rb[i] = *reinterpret_cast<const uint4*>(rr + at(i) + 4);
+        }
+    }
+  }
+  float p[P][8];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int left = k - at(i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[i][j] = 1.0f;
+    if (a.weight == nullptr) continue;
+    if (left >= 8) {
+      as_floats(*reinterpret_cast<const uint4*>(a.weight + at(i)), *reinterpret_cast<const uint4*>(a.weight + at(i) + 4), p[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) p[i][j] = a.weight[at(i) + j];
+    }
+  }
+
+  uint32_t mk = 0;
+  double ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int left = k - at(i);   // values of this piece inside the row
+    float s[8];
+    if (a.x_bf16) widen(xa[i], s);
+    else as_floats(xa[i], xb[i], s);
+    if (a.r != nullptr) {
+      float r[8];
+      if (a.r_bf16) {
+        widen(ra[i], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = s[j] + r[j];
+        const uint4 d = narrow(s);   // the stream's type holds the sum: what is normed is what is stored
+        widen(d, s);
+        if (a.sum_out != nullptr) {
+          uint16_t* o = static_cast<uint16_t*>(a.sum_out) + row * a.lds + at(i);
+          if (left >= 8) {
+            *reinterpret_cast<uint4*>(o) = d;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < left) o[j] = (uint16_t)(__float_as_uint(s[j]) >> 16);
+          }
+        }
+      } else {
+        as_floats(ra[i], rb[i], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = s[j] + r[j];
+        if (a.sum_out != nullptr) {
+          float* o = static_cast<float*>(a.sum_out) + row * a.lds + at(i);
+          if (left >= 8) {
+            *reinterpret_cast<f32x4*>(o) = f32x4{s[0], s[1], s[2], s[3]};
+            *reinterpret_cast<f32x4*>(o + 4) = f32x4{s[4], s[5], s[6], s[7]};
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < left) o[j] = s[j];
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s[j] = j < left ? s[j] : 0.0f;             // what lies past the row
+      ss = __builtin_fma((double)s[j], (double)s[j], ss);
+      p[i][j] = s[j] * p[i][j];
+      const uint32_t m = __float_as_uint(p[i][j]) & 0x7FFFFFFFu;
+      mk = m > mk ? m : mk;
+    }
+  }
+  // the normed row's factor needs the reductions, the selection does not: it runs while the other
+  // waves' arrive.  Dropped values are zeroed after the normed row is written: their bits wait.
+  uint32_t keep[SEL > 0 ? UN : 1][SEL == 4 ? 2 : 1];
+  if constexpr (SEL > 0) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int g = 0; g < (SEL == 4 ? 2 : 1); ++g) keep[u][g] = keep_bits<SEL, NK>(&p[u * PU][0] + g * SEL, a.n);
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)mk, off, 64);
+    mk = o > mk ? o : mk;
+    ss += __shfl_xor(ss, off, 64);
+  }
+  if constexpr (!WAVE) {
+    if ((threadIdx.x & 63) == 0) {
+      red_max[threadIdx.x >> 6] = mk;
+      red_sum[threadIdx.x >> 6] = ss;
+    }
+    __syncthreads();
+    mk = red_max[0];
+    ss = red_sum[0];
+    for (int w = 1; w < (int)(blockDim.x >> 6); ++w) {
+      mk = red_max[w] > mk ? red_max[w] : mk;
+      ss += red_sum[w];
+    }
+  }
+  const double rstd = 1.0 / __builtin_sqrt(ss / (double)(k > 0 ? k : 1) + (double)a.eps);
+  const RowCode rc = row_code(mk);
+  if (tid == 0) a.scale[row] = mk == 0 ? 1.0f : mk >= 0x7F800000u ? rc.amax : (float)((double)rc.amax * rstd / 127.0);
+  if (a.y != nullptr) {
+    const float f = (float)rstd;
+    uint16_t* yr = a.y + row * a.ldy;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int left = k - at(i);
+      if (left <= 0) continue;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = p[i][j] * f;
+      const uint4 d = narrow(v);
+      if (left >= 8) {
+        *reinterpret_cast<uint4*>(yr + at(i)) = d;
+      } else {
+        const uint32_t e[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left) yr[at(i) + j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  }
+  if constexpr (SEL > 0) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int e = 0; e < 8 * PU; ++e)
+        if (!((keep[u][SEL == 4 ? e / 4 : 0] >> (SEL == 4 ? e % 4 : e)) & 1u)) p[u * PU + e / 8][e % 8] = 0.0f;
+  }
+
+  int8_t* qr = a.q + row * a.ldq;
+  unsigned char* const row_codes = codes + (WAVE ? (threadIdx.x >> 6) * ((k + 15) / 16 * 16) : 0);
+  const int kq16 = (k + 15) / 16 * 16;   // written length of an unlifted row
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int k0 = at(i);
+    uint2 o = make_uint2(codes4(p[i], rc), codes4(p[i] + 4, rc));
+    if (rc.zero) o = make_uint2(0u, 0u);
+    if constexpr (LIFT == 0) {
+      if (k0 < kq16) *reinterpret_cast<uint2*>(qr + k0) = o;   // past k: zeros
+    } else if constexpr (LIFT == 4) {
+      // 8 values (k % 8 == 0) -> windows [0, 4), [2, 6), [4, 8)
+      if (k0 < k) {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(qr + k0 / 8 * 12);
+        dst[0] = o.x;
+        dst[1] = (o.x >> 16) | (o.y << 16);
+        dst[2] = o.y;
+      }
+    } else {
+      if (k0 < kq16) *reinterpret_cast<uint2*>(row_codes + k0) = o;
+    }
+  }
+  if constexpr (LIFT == 4) {
+    // zeros from 12 k / 8 up to a multiple of 16
+    const int kl = k / 8 * 12, kl16 = (kl + 15) / 16 * 16;
+    if (tid < (kl16 - kl) / 4) reinterpret_cast<uint32_t*>(qr + kl)[tid] = 0u;
+  }
+  if constexpr (LIFT == 1) {
+    if constexpr (WAVE) wave_lds_fence();
+    else __syncthreads();
+    const uint32_t wpg = (uint32_t)(a.ns - 1);
+    const int dwords = k / (2 * a.ns) * (a.ns - 1);
+    const int quads = (dwords + 3) / 4;
+    for (int i = tid; i < quads; i += NT) {
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t j = 4 * i + e, g = j / wpg, w = j - g * wpg;
+        o[e] = 0u;
+        if ((int)j < dwords) {
+          const uint16_t* s = reinterpret_cast<const uint16_t*>(row_codes + 2 * (a.ns * g + w));
+          o[e] = s[0] | ((uint32_t)s[1] << 16);
+        }
+      }
+      *reinterpret_cast<uint4*>(qr + 16 * (int64_t)i) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+template <bool WAVE, int UN, int SEL, int NK, int LIFT>
+hipError_t launch_n(int threads, const NormArgs& a, hipStream_t s) {
+  const size_t lds = LIFT == 1 ? (size_t)((a.k + 15) / 16 * 16) * (WAVE ? 4 : 1) : 0;
+  constexpr int64_t kRows = (1 << 22) - 4;   // of a launch: a grid holds under 2^32 threads
+  for (int64_t r = 0; r < a.rows; r += kRows) {
+    NormArgs b = a;
+    b.rows = a.rows - r < kRows ? a.rows - r : kRows;
+    b.x = static_cast<const char*>(a.x) + r * a.ldx * (a.x_bf16 ? 2 : 4);
+    if (a.r != nullptr) b.r = static_cast<const char*>(a.r) + r * a.ldr * (a.r_bf16 ? 2 : 4);
+    if (a.sum_out != nullptr) b.sum_out = static_cast<char*>(a.sum_out) + r * a.lds * (a.r_bf16 ? 2 : 4);
+    if (a.y != nullptr) b.y = a.y + r * a.ldy;
+    b.q = a.q + r * a.ldq;
+    b.scale = a.scale + r;
+    k_rmsnorm_i8<WAVE, UN, SEL, NK, LIFT>
+        <<<dim3((unsigned)(WAVE ? (b.rows + 3) / 4 : b.rows)), dim3(WAVE ? 256 : threads), lds, s>>>(b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// A row per wave up to 2048 values (4 pieces a lane); longer rows 2 pieces a thread up to 4096
+// values (4 for groups of 32, whose unit is 4), 4 beyond.
+template <int SEL, int NK, int LIFT>
+hipError_t by_length(const NormArgs& a, hipStream_t s) {
+  constexpr int PU = SEL > 8 ? SEL / 8 : 1;
+  if (a.k <= 2048) return launch_n<true, 4 / PU, SEL, NK, LIFT>(256, a, s);
+  const int pieces = PU <= 2 && a.k <= 4096 ? 2 : 4;
+  const int threads = (int)(((a.k + 15) / 16 * 16 + 512 * pieces - 1) / (512 * pieces) * 64);
+  if constexpr (PU <= 2) {
+    if (pieces == 2) return launch_n<false, 2 / PU, SEL, NK, LIFT>(threads, a, s);
+  }
+  return launch_n<false, 4 / PU, SEL, NK, LIFT>(threads, a, s);
+}
+
+}  // namespace
+
+namespace nml {
+
+hipError_t launch_rmsnorm_i8(const NormArgs& a, hipStream_t s) {
+  if (a.rows <= 0) return hipSuccess;
+  if (a.rows > 0x7FFFFFFF || a.k > 32768) return hipErrorInvalidValue;
+  if (a.ns == 4) return by_length<0, 0, 4>(a, s);
+  if (a.ns > 2) return by_length<0, 0, 1>(a, s);
+  switch (a.m) {
+    case 0: return by_length<0, 0, 0>(a, s);
+#define NM_CASE(M)                                      \
+  case M:                                               \
+    if (a.n == M / 2) return by_length<M, M / 2, 0>(a, s); \
+    return by_length<M, 0, 0>(a, s);
+    NM_CASE(4) NM_CASE(8) NM_CASE(16) NM_CASE(32)
+#undef NM_CASE
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace nml
