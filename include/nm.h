@@ -708,6 +708,61 @@ typedef enum { NM_ROUTER_SOFTMAX = 0, NM_ROUTER_SIGMOID = 1 } nm_router;
 nm_status nm_moe_route(const float* logits, int64_t t, int64_t experts, int64_t ldl, const float* bias, nm_router kind,
                        int top, int renormalize, float scale, int32_t* ids, float* weights, void* stream);
 
+/*
+ * nm_moe_i8 -- the experts' GLU MLPs of a few tokens in 8-bit integers:
+ *   h = bf16(act(gate_e x[t]) * up_e x[t])     (nm_glu_i8's values, for each expert e of token t)
+ *   y[t] = residual[t] + sum over the token's experts g_e (fp32(sum_i Q(h)[i] w_down_e[o][i]) hs) ds_e[o]
+ * Q(h), hs: nm_quant_i8's codes and scale of the row h.  The products' sums are exact in parts of a
+ * row, each part scaled; the parts and the experts are added in fp32 (in an order that depends on
+ * the call's sizes and ids alone), then the residual, and y is rounded once.
+ *   x         int8 [t][ldx], x_scale fp32 [t] (nm_rmsnorm_i8, nm_quant_i8), rows as for nm_spmm_i8
+ *   ids       int32 [t][top], weights fp32 [t][top] (nm_moe_route): the token's experts.  An id
+ *             outside [0, experts) is none (a token without any: y = residual); one that occurs
+ *             twice counts with both weights
+ *   w_gate, w_up   int8 [experts][inter][ldw], scales fp32 [experts][inter]
+ *   w_down    int8 [experts][hidden][ldd], scales fp32 [experts][hidden]
+ *   *_meta    all NULL: dense weights; all given: 2:4 over hidden, hidden and inter (both % 4 ==
+ *             0): an expert's kept values as nm_compress orders them and its positions as
+ *             nm_meta_block lays them out, one expert behind the other
+ *   residual  of y's type, [t][ldr], or NULL; may be y with ldr = ldy; otherwise no overlap
+ *   y         NM_Y_F32 or NM_Y_BF16, [t][ldy]
+ *   workspace nm_moe_i8_workspace_size bytes (NM_EINVAL if less); contents after the call are
+ *             unspecified; calls sharing a workspace must be ordered
+ * Every 64 tokens are a pass over the weights of the experts that they ask for: meant for up to
+ * some hundred tokens.  hidden <= NM_I8_MAX_K, inter <= 65536, experts <= NM_MOE_MAX_EXPERTS, top <=
+ * NM_MOE_MAX_TOP (NM_EUNSUPPORTED above).
+ */
+typedef struct {
+  int64_t t, hidden, inter;
+  int experts, top;
+  const int8_t* x;
+  int64_t ldx;             /* bytes, % 16 == 0                                      */
+  const float* x_scale;
+  const int32_t* ids;
+  const float* weights;
+  const int8_t* w_gate;
+  const int8_t* w_up;
+  int64_t ldw;             /* bytes, % 16 == 0: hidden, or hidden / 2 (2:4)         */
+  const float* gate_scale;
+  const float* up_scale;
+  const void* gate_meta;
+  const void* up_meta;
+  const int8_t* w_down;
+  int64_t ldd;             /* bytes, % 16 == 0: inter, or inter / 2 (2:4)           */
+  const float* down_scale;
+  const void* down_meta;
+  nm_glu_act act;
+  const void* residual;
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  nm_ydtype y_dtype;
+  void* workspace;
+  int64_t workspace_bytes;
+} nm_moe_args;
+nm_status nm_moe_i8(const nm_moe_args* args, void* stream);
+int64_t nm_moe_i8_workspace_size(int64_t t, int64_t experts, int64_t top, int64_t hidden, int64_t inter, int sparse);
+
 #ifdef __cplusplus
 }
 #endif

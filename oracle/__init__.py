@@ -913,3 +913,59 @@ def moe_route(logits: np.ndarray, top: int, sigmoid: bool = False, bias=None, re
         if renormalize:
             weights[r] = weights[r] / whole if whole > 0 else 0.0
     return ids, weights * float(np.float32(scale))
+
+
+def gate_error(g: np.ndarray, act: str) -> np.ndarray:
+    """Relative error, in units of 2^-24, of a gate computed in fp32 from a g that is itself 3 units
+    off: the gate's logarithm moves by at most 1 + 3 |z| of g's (z: the exponent), the exponent's own
+    rounding by |z|, the rest by a few."""
+    z = np.abs(g if act == "silu" else 2.0 * np.sqrt(2.0 / np.pi) * (g + 0.044715 * g ** 3))
+    return 3 * (1 + 3 * z) + 4 * z + 12
+
+
+def moe_i8(x, x_scale, ids, weights, gate, up, down, act: str = "silu", residual=None):
+    """fp64 y [T][H] of the experts' MLPs; how far a computation whose gates are in fp32 may be from it for
+    that alone; and the sums of all terms' magnitudes, for what adding them rounds.  x int8 [T][H]; gate, up, down: (codes [E][rows][k] expanded, scales
+    [E][rows]).  h = bf16(act(g) u) of the exact sums; its codes and scale as nm_quant_i8 has them.
+    An h next to a border of bf16 may fall on its other side, and with it its code, or, as the
+    row's largest, all of them: the second result
+    follows both sides."""
+    t = x.shape[0]
+    rows = down[0].shape[1]
+    y = np.zeros((t, rows)) if residual is None else np.asarray(residual, np.float64).copy()
+    far = np.zeros((t, rows))
+    size = np.abs(y)
+    e_all = gate[0].shape[0]
+    for r in range(t):
+        for j in range(ids.shape[1]):
+            e = int(ids[r, j])
+            if e < 0 or e >= e_all:
+                continue
+            xr = x[r].astype(np.float64)
+            g = (gate[0][e].astype(np.float64) @ xr) * np.float64(x_scale[r]) * gate[1][e]
+            u = (up[0][e].astype(np.float64) @ xr) * np.float64(x_scale[r]) * up[1][e]
+            h = glu_gate(g, act) * u
+            off = (gate_error(g, act) + 5) * 2.0 ** -24
+
+            def coded(v, top):
+                if not np.isfinite(top):
+                    return np.zeros_like(v), np.float64(top)
+                if top == 0:
+                    return np.zeros_like(v), np.float64(1)
+                return np.rint(127.0 * v / top), np.float64(np.float32(top / 127.0))
+
+            sides = [bf16_round((h * (1 + s * off)).astype(np.float32)).astype(np.float64) for s in (-1, 0, 1)]
+            tops = [np.abs(v).max() if v.size else 0.0 for v in sides]
+            q, s = coded(sides[1], tops[1])
+            dv = np.zeros_like(h)
+            for v in sides:
+                for top in tops:
+                    top = max(top, np.abs(v).max() if v.size else 0.0)
+                    qq, ss = coded(v, top)
+                    dv = np.maximum(dv, np.abs(qq * ss - q * s))
+            w = down[0][e].astype(np.float64)
+            f = np.float64(weights[r, j]) * down[1][e]
+            y[r] += f * (w @ q) * s
+            far[r] += np.abs(f) * (np.abs(w) @ dv)
+            size[r] += np.abs(f) * (np.abs(w) @ np.abs(q)) * s
+    return y, far, size

@@ -27,7 +27,7 @@ __all__ = [
     "NM_PTS_STATIC", "NM_PTS_VAR", "nm_sparsify_pts", "nm_weight_sums", "NM_ESCRATCH", "nm_spmm_noalloc",
     "NM_NOALLOC_SCRATCH_BYTES", "nm_quant_i8", "nm_meta_block", "nm_meta_block_bytes", "nm_spmm_i8", "nm_glu_i8",
     "nm_i8_workspace_size", "NM_I8_MAX_K", "NM_I8_MAX_ROWS", "NM_Y_F32", "NM_Y_BF16", "NM_GLU_SILU", "NM_GLU_GELU_TANH",
-    "nm_rmsnorm_i8", "nm_moe_route", "NM_MOE_MAX_EXPERTS", "NM_MOE_MAX_TOP", "NM_ROUTER_SOFTMAX", "NM_ROUTER_SIGMOID",
+    "nm_rmsnorm_i8", "nm_moe_route", "nm_moe_i8", "nm_moe_i8_workspace_size", "nm_moe_args", "NM_MOE_MAX_EXPERTS", "NM_MOE_MAX_TOP", "NM_ROUTER_SOFTMAX", "NM_ROUTER_SIGMOID",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnmsparse.so")
@@ -87,6 +87,18 @@ class nm_spmm_args(ctypes.Structure):
         ("route", ctypes.c_uint32), ("few_wpb", ctypes.c_int32), ("few_splits", ctypes.c_int32),
         ("tile_wg", ctypes.c_int32), ("route_taken", _vp),
         ("pts", _int), ("pts_shift", _vp), ("col_shift", _vp), ("row_scale", _vp), ("row_shift", _vp),
+    ]
+
+
+class nm_moe_args(ctypes.Structure):
+    _fields_ = [
+        ("t", _i64), ("hidden", _i64), ("inter", _i64), ("experts", _int), ("top", _int),
+        ("x", _vp), ("ldx", _i64), ("x_scale", _vp), ("ids", _vp), ("weights", _vp),
+        ("w_gate", _vp), ("w_up", _vp), ("ldw", _i64), ("gate_scale", _vp), ("up_scale", _vp),
+        ("gate_meta", _vp), ("up_meta", _vp),
+        ("w_down", _vp), ("ldd", _i64), ("down_scale", _vp), ("down_meta", _vp),
+        ("act", _int), ("residual", _vp), ("ldr", _i64), ("y", _vp), ("ldy", _i64), ("y_dtype", _int),
+        ("workspace", _vp), ("workspace_bytes", _i64),
     ]
 
 
@@ -177,6 +189,10 @@ def lib() -> ctypes.CDLL:
                                 _int, _vp, _i64, _vp, _i64, _vp, _vp]
     L.nm_moe_route.restype = _int
     L.nm_moe_route.argtypes = [_vp, _i64, _i64, _i64, _vp, _int, _int, _int, ctypes.c_float, _vp, _vp, _vp]
+    L.nm_moe_i8.restype = _int
+    L.nm_moe_i8.argtypes = [ctypes.POINTER(nm_moe_args), _vp]
+    L.nm_moe_i8_workspace_size.restype = _i64
+    L.nm_moe_i8_workspace_size.argtypes = [_i64, _i64, _i64, _i64, _i64, _int]
     _LIB = L
     return L
 
@@ -828,3 +844,82 @@ def nm_moe_route(logits, ids, weights, kind=NM_ROUTER_SOFTMAX, bias=None, renorm
     if check and res:
         _check(res, "nm_moe_route")
     return res
+
+
+def _expert_codes(w, dev, experts, rows, cols, ld, name):
+    """(pointer, leading dimension) of int8 weights [experts][rows][ld], read in pieces of 16: a 3-D tensor
+    whose experts follow each other without a gap, or a matrix of all their rows."""
+    if w is None or type(w) is int:
+        return w, ld or 0
+    st, sh = w.stride(), w.shape
+    if experts * rows * cols == 0 and w.get_device() == dev:    # nothing of it is read
+        return w.data_ptr(), ld or cols + -cols % 16
+    if w.get_device() != dev or w.dtype not in _int8s or len(st) not in (2, 3) or st[-1] != 1:
+        _refuse(w, dev, f"{name}: rows of int8 codes are needed")
+    if ld is None:
+        ld = st[-2]
+    if len(st) == 3 and (sh[0] < experts or sh[1] != rows or (sh[0] > 1 and st[0] != rows * st[1]) or ld != st[1]):
+        raise ValueError(f"{name}: {experts} experts of {rows} rows, one behind the other, are needed")
+    if len(st) == 2 and (sh[0] < experts * rows or ld != st[0]):
+        raise ValueError(f"{name}: {experts * rows} rows are needed")
+    if sh[-1] + -sh[-1] % 16 < cols:
+        raise ValueError(f"{name}: rows of {cols} codes are needed")
+    if experts * rows > 0 and cols > 0:
+        end = w.storage_offset() + (experts * rows - 1) * ld + cols + -cols % 16
+        if end > w.untyped_storage().nbytes():
+            raise ValueError(f"{name}: the storage ends inside the last row")
+    return w.data_ptr(), ld
+
+
+def nm_moe_i8(x, x_scale, ids, weights, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, y, act=NM_GLU_SILU,
+              gate_meta=None, up_meta=None, down_meta=None, residual=None, workspace=None, stream=None, *, t=None,
+              experts=None, top=None, hidden=None, inter=None, ldx=None, ldw=None, ldd=None, ldr=None, ldy=None,
+              y_dtype=None, workspace_bytes=None, check=True):
+    """y = residual + the weighted sum of each token's experts' GLU MLPs, in 8-bit integers (include/nm.h).
+    ids, weights: [t][top] as nm_moe_route writes them; w_gate, w_up int8 [experts][inter][..], w_down
+    int8 [experts][hidden][..]; hidden, inter: where they are not y's width and w_gate's rows."""
+    if stream is None:
+        dev, stream = _current()
+    else:
+        dev, stream = _device_of(x, y, w_gate, w_up, w_down, ids, weights, x_scale, gate_scale, up_scale, down_scale,
+                                 gate_meta, up_meta, down_meta, residual, workspace), _stream(stream)
+    if t is None:
+        t = x.shape[0]
+    if experts is None:
+        experts = w_gate.shape[0]
+    if top is None:
+        top = ids.shape[1]
+    if hidden is None:
+        hidden = y.shape[1]
+    if inter is None:
+        inter = w_gate.shape[1]
+    sparse = gate_meta is not None
+    wk, dk = (hidden // 2, inter // 2) if sparse else (hidden, inter)
+    a = nm_moe_args()
+    a.t, a.hidden, a.inter, a.experts, a.top, a.act = t, hidden, inter, experts, top, act
+    a.x, a.ldx = _codes(x, None if x is None or type(x) is int else x.shape, dev, t, hidden, ldx)
+    a.x_scale = _list_of(x_scale, t, dev, _f32s, "x_scale")
+    a.ids = _list_of(ids, t * top, dev, _int32s, "ids")
+    a.weights = _list_of(weights, t * top, dev, _f32s, "weights")
+    a.w_gate, a.ldw = _expert_codes(w_gate, dev, experts, inter, wk, ldw, "w_gate")
+    a.w_up, lu = _expert_codes(w_up, dev, experts, inter, wk, ldw, "w_up")
+    if lu != a.ldw:
+        raise ValueError("w_gate and w_up need the same leading dimension")
+    a.w_down, a.ldd = _expert_codes(w_down, dev, experts, hidden, dk, ldd, "w_down")
+    a.gate_scale = _list_of(gate_scale, experts * inter, dev, _f32s, "gate_scale")
+    a.up_scale = _list_of(up_scale, experts * inter, dev, _f32s, "up_scale")
+    a.down_scale = _list_of(down_scale, experts * hidden, dev, _f32s, "down_scale")
+    a.gate_meta = _meta(gate_meta, experts * inter, hidden, dev)
+    a.up_meta = _meta(up_meta, experts * inter, hidden, dev)
+    a.down_meta = _meta(down_meta, experts * hidden, inter, dev)
+    a.y, a.ldy, a.y_dtype = _rows_of(y, dev, t, hidden, 1, ldy, y_dtype, "y")
+    a.residual, a.ldr, _ = _rows_of(residual, dev, t, hidden, 1, ldr, a.y_dtype, "residual")
+    a.workspace, a.workspace_bytes = _scratch(workspace, workspace_bytes, dev)
+    res = lib().nm_moe_i8(a, stream)
+    if check and res:
+        _check(res, "nm_moe_i8")
+    return res
+
+
+def nm_moe_i8_workspace_size(t: int, experts: int, top: int, hidden: int, inter: int, sparse: bool = False) -> int:
+    return int(lib().nm_moe_i8_workspace_size(t, experts, top, hidden, inter, 1 if sparse else 0))

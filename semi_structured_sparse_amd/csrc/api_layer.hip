@@ -1,5 +1,5 @@
 // C ABI of the operators around the products: host-side validation and dispatch
-// (nm_rmsnorm_i8, nm_moe_route).  Arguments are checked completely before the first HIP call.
+// (nm_rmsnorm_i8, nm_moe_route, nm_moe_i8).  Arguments are checked completely before the first HIP call.
 #include "layer_launch.h"
 
 namespace {
@@ -68,6 +68,59 @@ nm_status nm_moe_route(const float* logits, int64_t t, int64_t experts, int64_t 
   if (experts > NM_MOE_MAX_EXPERTS || top > NM_MOE_MAX_TOP || t > (1 << 25)) return NM_EUNSUPPORTED;
   const nml::RouteArgs a{logits, bias, ids, weights, t, experts, ldl, top, kind == NM_ROUTER_SIGMOID, renormalize, scale};
   return hip_status(nml::launch_moe_route(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+nm_status nm_moe_i8(const nm_moe_args* args, void* stream) {
+  if (args == nullptr) return NM_EINVAL;
+  const nm_moe_args& g = *args;
+  if (g.act != NM_GLU_SILU && g.act != NM_GLU_GELU_TANH) return NM_EINVAL;
+  if (!is_dtype(g.y_dtype) || g.top < 1 || g.experts < 1) return NM_EINVAL;
+  const bool sp = g.gate_meta != nullptr;
+  if ((g.up_meta != nullptr) != sp || (g.down_meta != nullptr) != sp) return NM_EINVAL;
+  if (g.t < 0 || g.hidden < 0 || g.inter < 0 || g.workspace_bytes < 0) return NM_ESHAPE;
+  if (sp && (g.hidden % 4 != 0 || g.inter % 4 != 0)) return NM_ESHAPE;
+  const int64_t wk = sp ? g.hidden / 2 : g.hidden, dk = sp ? g.inter / 2 : g.inter;
+  if (g.ldx < g.hidden || g.ldw < wk || g.ldd < dk || g.ldy < g.hidden || (g.residual != nullptr && g.ldr < g.hidden))
+    return NM_ESHAPE;
+  int64_t rows_i, rows_h;
+  if (__builtin_mul_overflow((int64_t)g.experts, g.inter, &rows_i) ||
+      __builtin_mul_overflow((int64_t)g.experts, g.hidden, &rows_h) || !span_ok(rows_i, g.ldw) || !span_ok(rows_h, g.ldd) ||
+      !span_ok(rows_i, g.hidden) || !span_ok(rows_h, g.inter) || !span_ok(g.t, g.ldx) || !span_ok(g.t, g.ldy) ||
+      !span_ok(g.t, g.top) || (g.residual != nullptr && !span_ok(g.t, g.ldr)))
+    return NM_ESHAPE;
+  const bool some = g.t > 0 && g.hidden > 0;
+  if (some && (g.y == nullptr || g.ids == nullptr || g.weights == nullptr)) return NM_EINVAL;
+  if (some && g.inter > 0 &&
+      (g.x == nullptr || g.x_scale == nullptr || g.w_gate == nullptr || g.w_up == nullptr || g.w_down == nullptr ||
+       g.gate_scale == nullptr || g.up_scale == nullptr || g.down_scale == nullptr))
+    return NM_EINVAL;
+  if (g.ldx % 16 != 0 || g.ldw % 16 != 0 || g.ldd % 16 != 0) return NM_EALIGN;
+  if (!all_aligned(g.x, g.x_scale, g.ids, g.weights, g.w_gate, g.w_up, g.gate_scale, g.up_scale, g.gate_meta, g.up_meta,
+                   g.w_down, g.down_scale, g.down_meta, g.residual, g.y, g.workspace))
+    return NM_EALIGN;
+  if (g.hidden > NM_I8_MAX_K || g.inter > 65536 || g.experts > NM_MOE_MAX_EXPERTS || g.top > NM_MOE_MAX_TOP)
+    return NM_EUNSUPPORTED;
+  if (!some) return NM_OK;
+  if (g.workspace == nullptr || g.workspace_bytes < nml::moe_workspace_bytes(g.t, g.top, g.inter)) return NM_EINVAL;
+  nml::MoeArgs a{};
+  a.x = g.x; a.x_scale = g.x_scale; a.ids = g.ids; a.weights = g.weights;
+  a.w_gate = g.w_gate; a.w_up = g.w_up; a.w_down = g.w_down;
+  a.gate_scale = g.gate_scale; a.up_scale = g.up_scale; a.down_scale = g.down_scale;
+  a.gate_meta = static_cast<const uint8_t*>(g.gate_meta);
+  a.up_meta = static_cast<const uint8_t*>(g.up_meta);
+  a.down_meta = static_cast<const uint8_t*>(g.down_meta);
+  a.residual = g.residual; a.y = g.y;
+  a.ldx = g.ldx; a.ldw = g.ldw; a.ldd = g.ldd; a.ldr = g.ldr; a.ldy = g.ldy;
+  a.t = g.t; a.hidden = g.hidden; a.inter = g.inter;
+  a.experts = g.experts; a.top = g.top; a.act = (int)g.act; a.bf16_out = g.y_dtype == NM_Y_BF16;
+  return hip_status(nml::launch_moe_i8(a, g.workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int64_t nm_moe_i8_workspace_size(int64_t t, int64_t experts, int64_t top, int64_t hidden, int64_t inter, int sparse) {
+  (void)sparse;
+  if (t <= 0 || experts <= 0 || top <= 0 || hidden <= 0 || inter < 0) return 0;
+  if (hidden > NM_I8_MAX_K || inter > 65536 || experts > NM_MOE_MAX_EXPERTS || top > NM_MOE_MAX_TOP) return 0;
+  return nml::moe_workspace_bytes(t, top, inter);
 }
 
 }  // extern "C"

@@ -4,7 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "nm_launch.h"
+#include "i8_launch.h"
 
 namespace nml {
 
@@ -33,5 +33,24 @@ struct RouteArgs {
   float scale;
 };
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s);
+
+// The experts' MLPs of a few tokens.  Weights: row o of expert e at (e rows + o) ld bytes; 2:4
+// positions of an expert [ceil(k/128)][rows][16].
+struct MoeArgs {
+  const int8_t* x;
+  const float* x_scale;
+  const int32_t* ids;       // [t][top]
+  const float* weights;
+  const int8_t *w_gate, *w_up, *w_down;
+  const float *gate_scale, *up_scale, *down_scale;
+  const uint8_t *gate_meta, *up_meta, *down_meta;   // all null: dense
+  const void* residual;     // of y's type, or null
+  void* y;
+  int64_t ldx, ldw, ldd, ldr, ldy;
+  int64_t t, hidden, inter;
+  int experts, top, act, bf16_out;
+};
+int64_t moe_workspace_bytes(int64_t t, int64_t top, int64_t inter);
+hipError_t launch_moe_i8(const MoeArgs& a, void* ws, hipStream_t s);
 
 }  // namespace nml
