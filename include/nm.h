@@ -684,6 +684,41 @@ nm_status nm_rmsnorm_i8(const void* x, nm_ydtype x_dtype, int64_t rows, int64_t 
                         int64_t ldr, void* sum_out, int64_t lds, nm_ydtype stream_dtype, const float* weight, float eps,
                         int n, int m, int ns, void* y, int64_t ldy, int8_t* q, int64_t ldq, float* scale, void* stream);
 
+typedef enum { NM_FN_NONE = 0, NM_FN_RELU = 1, NM_FN_SILU = 2, NM_FN_GELU_TANH = 3 } nm_fn;
+#define NM_LINEAR_MAX_K (1 << 24)
+#define NM_LINEAR_MAX_ROWS 134217728
+
+/*
+ * nm_linear -- the linear layer in bf16 with its epilogue, one pass over the output:
+ *   y[t][o] = residual[t][o] + fn(sum_k x[t][k] w[o][k] + bias[o])
+ * Sums, bias, activation and the residual's addition in fp32, y rounded once (to nearest even).
+ *   x         bf16 [t][ldx], any k >= 0; ldx % 8 == 0, rows readable up to a multiple of 8 values
+ *             (what lies past k may hold anything, NaN included; so for w)
+ *   w         w_meta NULL: bf16 [o][ldw], dense.  Otherwise 2:4 over k (k % 4 == 0): the kept values
+ *             bf16 [o][ldw >= k/2] in nm_compress's order, w_meta their positions in step blocks
+ *             (nm_meta_block), as nm_spmm_i8 takes them; on the sparse matrix instruction
+ *   bias      fp32 [o] or NULL
+ *   fn        relu: max(v, 0); silu: v / (1 + e^-v); gelu: v (1 + tanh(sqrt(2/pi) (v + 0.044715
+ *             v^3))) / 2; a NaN stays NaN
+ *   residual  of y's type, [t][ldr >= o], or NULL; may be y with ldr = ldy, otherwise no overlap
+ *   y         NM_Y_F32 or NM_Y_BF16, [t][ldy >= o]; nothing outside rows [0, t) and columns [0, o) is
+ *             written
+ *   workspace device scratch or NULL.  With nm_linear_workspace_size bytes the reduction may be
+ *             split across workgroups; with less, the call runs unsplit.  Contents after the
+ *             call are unspecified; calls sharing a workspace must be ordered.
+ *   route, route_taken   as for nm_spmm_i8
+ * k == 0 gives zero sums (x and w may then be NULL).  The same call on the same inputs gives the same
+ * bits; routes differ in the order of their fp32 sums.  k <= NM_LINEAR_MAX_K, t and o <=
+ * NM_LINEAR_MAX_ROWS (NM_EUNSUPPORTED above).
+ */
+nm_status nm_linear(const void* x, int64_t t, int64_t k, int64_t ldx, const void* w, int64_t o, int64_t ldw,
+                    const void* w_meta, const float* bias, nm_fn fn, const void* residual, int64_t ldr, void* y,
+                    int64_t ldy, nm_ydtype y_dtype, void* workspace, int64_t workspace_bytes, uint32_t route,
+                    uint32_t* route_taken, void* stream);
+
+/* Workspace bytes of nm_linear's preferred route. */
+int64_t nm_linear_workspace_size(int64_t t, int64_t o, int64_t k, int sparse, uint32_t route);
+
 #define NM_MOE_MAX_EXPERTS 1024
 #define NM_MOE_MAX_TOP 32
 

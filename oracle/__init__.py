@@ -969,3 +969,26 @@ def moe_i8(x, x_scale, ids, weights, gate, up, down, act: str = "silu", residual
             far[r] += np.abs(f) * (np.abs(w) @ dv)
             size[r] += np.abs(f) * (np.abs(w) @ np.abs(q)) * s
     return y, far, size
+
+
+def linear(x: np.ndarray, w: np.ndarray, bias=None, fn: str = "none", residual=None):
+    """fp64 (y, |x| |w|^T): y = residual + fn(x w^T + bias) of values x [T][K], w [O][K]."""
+    x, w = np.asarray(x, np.float64), np.asarray(w, np.float64)
+    v = x @ w.T
+    size = np.abs(x) @ np.abs(w).T
+    if bias is not None:
+        v = v + np.asarray(bias, np.float64)[None, :]
+    if fn == "relu":
+        v = np.where(v < 0, 0.0, v)
+    elif fn != "none":
+        v = glu_gate(v, fn)
+    return (v if residual is None else v + np.asarray(residual, np.float64)), size
+
+
+def expand_24_values(vals: np.ndarray, idx: np.ndarray, kc: int) -> np.ndarray:
+    """2:4 kept values [O][kc/2] with in-group positions idx -> dense [O][kc] of the same type."""
+    o = vals.shape[0]
+    w = np.zeros((o, kc), vals.dtype)
+    for j in range(kc // 2):
+        w[np.arange(o), 4 * (j // 2) + idx[:, j].astype(np.int64)] = vals[:, j]
+    return w

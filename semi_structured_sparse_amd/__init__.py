@@ -27,7 +27,8 @@ __all__ = [
     "NM_PTS_STATIC", "NM_PTS_VAR", "nm_sparsify_pts", "nm_weight_sums", "NM_ESCRATCH", "nm_spmm_noalloc",
     "NM_NOALLOC_SCRATCH_BYTES", "nm_quant_i8", "nm_meta_block", "nm_meta_block_bytes", "nm_spmm_i8", "nm_glu_i8",
     "nm_i8_workspace_size", "NM_I8_MAX_K", "NM_I8_MAX_ROWS", "NM_Y_F32", "NM_Y_BF16", "NM_GLU_SILU", "NM_GLU_GELU_TANH",
-    "nm_rmsnorm_i8", "nm_moe_route", "nm_moe_i8", "nm_moe_i8_workspace_size", "nm_moe_args", "NM_MOE_MAX_EXPERTS", "NM_MOE_MAX_TOP", "NM_ROUTER_SOFTMAX", "NM_ROUTER_SIGMOID",
+    "nm_linear", "nm_linear_workspace_size", "NM_FN_NONE", "NM_FN_RELU", "NM_FN_SILU", "NM_FN_GELU_TANH",
+    "NM_LINEAR_MAX_K", "NM_LINEAR_MAX_ROWS", "nm_rmsnorm_i8", "nm_moe_route", "nm_moe_i8", "nm_moe_i8_workspace_size", "nm_moe_args", "NM_MOE_MAX_EXPERTS", "NM_MOE_MAX_TOP", "NM_ROUTER_SOFTMAX", "NM_ROUTER_SIGMOID",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnmsparse.so")
@@ -44,6 +45,8 @@ NM_I8_MAX_K = 131071
 NM_I8_MAX_ROWS = 1 << 27
 NM_Y_F32, NM_Y_BF16 = 0, 1
 NM_GLU_SILU, NM_GLU_GELU_TANH = 0, 1
+NM_FN_NONE, NM_FN_RELU, NM_FN_SILU, NM_FN_GELU_TANH = 0, 1, 2, 3
+NM_LINEAR_MAX_K, NM_LINEAR_MAX_ROWS = 1 << 24, 134217728
 NM_MOE_MAX_EXPERTS, NM_MOE_MAX_TOP = 1024, 32
 NM_ROUTER_SOFTMAX, NM_ROUTER_SIGMOID = 0, 1
 
@@ -184,6 +187,11 @@ def lib() -> ctypes.CDLL:
                             _int, _vp, _i64, ctypes.c_uint32, _vp, _vp]
     L.nm_i8_workspace_size.restype = _i64
     L.nm_i8_workspace_size.argtypes = [_i64, _i64, _i64, _int, _int, ctypes.c_uint32]
+    L.nm_linear.restype = _int
+    L.nm_linear.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _int, _vp, _i64, _vp, _i64, _int, _vp, _i64,
+                            ctypes.c_uint32, _vp, _vp]
+    L.nm_linear_workspace_size.restype = _i64
+    L.nm_linear_workspace_size.argtypes = [_i64, _i64, _i64, _int, ctypes.c_uint32]
     L.nm_rmsnorm_i8.restype = _int
     L.nm_rmsnorm_i8.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, ctypes.c_float, _int, _int,
                                 _int, _vp, _i64, _vp, _i64, _vp, _vp]
@@ -784,6 +792,53 @@ def _list_of(t, n, dev, types, name):
     if t.get_device() != dev or t.dtype not in types or t.numel() < n or not t.is_contiguous():
         _refuse(t, dev, f"{name}: {n} contiguous values are needed")
     return t.data_ptr()
+
+
+def _bf16_rows(t, dev, rows, cols, ld, name):
+    """(pointer, leading dimension) of `rows` rows of `cols` bf16 values that are read in pieces of 8."""
+    if t is None or type(t) is int:
+        return t, ld or 0
+    st, sh = t.stride(), t.shape
+    if len(st) != 2 or st[1] != 1 or t.get_device() != dev or t.dtype not in _bf16s:
+        _refuse(t, dev, f"{name}: a matrix with contiguous rows of bf16 values is needed")
+    if ld is None:
+        ld = st[0] if cols else 0       # of no columns: torch has 1
+    if sh[0] < rows or sh[1] < cols + -cols % 8 or ld != st[0]:
+        _holds(t, rows, cols, 8, ld)
+    return t.data_ptr(), ld
+
+
+def nm_linear(x, w, y, w_meta=None, bias=None, fn=NM_FN_NONE, residual=None, workspace=None, stream=None, *, t=None, o=None,
+              k=None, ldx=None, ldw=None, ldr=None, ldy=None, y_dtype=None, workspace_bytes=None, route=0, taken=None,
+              check=True):
+    """y = residual + fn(x . w^T + bias) in bf16 with fp32 sums; w_meta (from nm_meta_block): w holds the
+    kept values of 2:4 rows.  k: the reduction length where it is not x's width.
+    taken: optional ctypes.c_uint32 that receives the NM_TAKEN_* report."""
+    if stream is None:
+        dev, stream = _current()
+    else:
+        dev, stream = _device_of(x, w, y, w_meta, bias, residual, workspace), _stream(stream)
+    if t is None:
+        t = x.shape[0]
+    if o is None:
+        o = w.shape[0]
+    if k is None:
+        k = x.shape[1]
+    xp, lx = _bf16_rows(x, dev, t, k, ldx, "x")
+    wp, lw = _bf16_rows(w, dev, o, k if w_meta is None else k // 2, ldw, "w")
+    yp, ly, yd = _rows_of(y, dev, t, o, 1, ldy, y_dtype, "y")
+    rp, lr = (None, 0) if residual is None else _rows_of(residual, dev, t, o, 1, ldr, yd, "residual")[:2]
+    wsp, wsn = _scratch(workspace, workspace_bytes, dev)
+    res = lib().nm_linear(xp, t, k, lx, wp, o, lw, _meta(w_meta, o, k, dev),
+                          None if bias is None else _list_of(bias, o, dev, _f32s, "bias"), fn, rp, lr, yp, ly, yd, wsp, wsn,
+                          route, ctypes.addressof(taken) if taken is not None else None, stream)
+    if check and res:
+        _check(res, "nm_linear")
+    return res
+
+
+def nm_linear_workspace_size(t: int, o: int, k: int, sparse: bool = False, route: int = 0) -> int:
+    return int(lib().nm_linear_workspace_size(t, o, k, 1 if sparse else 0, route))
 
 
 def nm_rmsnorm_i8(x, weight, q, scale, residual=None, sum_out=None, y=None, eps=1e-6, n=0, m=0, ns=2, stream=None, *,

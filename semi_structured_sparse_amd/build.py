@@ -14,7 +14,7 @@ BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["api.hip", "select.hip", "slide.hip", "gemm_dense.hip", "gemm_lds.hip", "gemm_sparse.hip",
            "gemm_lds_sp.hip", "hybrid_pack.hip", "spense.hip", "decode.hip", "pts.hip",
            "api_i8.hip", "quant_i8.hip", "few_i8.hip", "gemm_i8.hip",
-           "api_layer.hip", "norm_i8.hip", "route.hip", "moe_i8.hip"]
+           "api_layer.hip", "linear_few.hip", "linear_tile.hip", "norm_i8.hip", "route.hip", "moe_i8.hip"]
 # measurement helpers live in a library of their own (not exported by libnmsparse)
 PROBE_SOURCES = ["probe.hip"]
 PROBE_OUT = os.path.join(PKG, "libnmprobe.so")

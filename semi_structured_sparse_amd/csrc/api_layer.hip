@@ -1,5 +1,5 @@
 // C ABI of the operators around the products: host-side validation and dispatch
-// (nm_rmsnorm_i8, nm_moe_route, nm_moe_i8).  Arguments are checked completely before the first HIP call.
+// (nm_linear, nm_rmsnorm_i8, nm_moe_route, nm_moe_i8).  Arguments are checked completely before the first HIP call.
 #include "layer_launch.h"
 
 namespace {
@@ -23,9 +23,58 @@ nm_status hip_status(hipError_t e) { return e == hipSuccess ? NM_OK : NM_EHIP; }
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
+enum class Kind { kFew, kMid, kLarge };
+
+// Up to 32 tokens the streaming kernel, whose row blocks need no partial sums; above, 256 x 256
+// tiles where there are enough of them to fill the chip, smaller tiles below.
+Kind plan_linear(int64_t t, int64_t o, int64_t k, uint32_t route) {
+  if (route & NM_ROUTE_FEW_STREAM) return Kind::kFew;
+  if (route & NM_ROUTE_FEW_TILE) return Kind::kMid;
+  if (route & NM_ROUTE_TILE_LDS) return Kind::kLarge;
+  if (t <= 32) return (o + 63) / 64 >= 192 || (t > 8 && t * k > 8 * 8192) ? Kind::kMid : Kind::kFew;
+  return ((o + 255) / 256) * ((t + 255) / 256) >= 160 ? Kind::kLarge : Kind::kMid;
+}
+
 }  // namespace
 
 extern "C" {
+
+nm_status nm_linear(const void* x, int64_t t, int64_t k, int64_t ldx, const void* w, int64_t o, int64_t ldw,
+                    const void* w_meta, const float* bias, nm_fn fn, const void* residual, int64_t ldr, void* y,
+                    int64_t ldy, nm_ydtype y_dtype, void* workspace, int64_t workspace_bytes, uint32_t route,
+                    uint32_t* route_taken, void* stream) {
+  if (!is_dtype(y_dtype) || fn < NM_FN_NONE || fn > NM_FN_GELU_TANH) return NM_EINVAL;
+  if (t < 0 || o < 0 || k < 0 || workspace_bytes < 0) return NM_ESHAPE;
+  const bool sp = w_meta != nullptr, some = t > 0 && o > 0;
+  if (sp && k % 4 != 0) return NM_ESHAPE;
+  if (some && (y == nullptr || (k > 0 && (x == nullptr || w == nullptr)))) return NM_EINVAL;
+  if (ldx < k || ldw < (sp ? k / 2 : k) || ldy < o || (residual != nullptr && ldr < o)) return NM_ESHAPE;
+  if (!span_ok(t, ldx) || !span_ok(o, ldw) || !span_ok(t, ldy) || !span_ok(t, o) || (sp && !span_ok(o, k)) ||
+      (residual != nullptr && !span_ok(t, ldr)))
+    return NM_ESHAPE;
+  if (ldx % 8 != 0 || ldw % 8 != 0 || !all_aligned(x, w, w_meta, bias, residual, y, workspace)) return NM_EALIGN;
+  if (k > NM_LINEAR_MAX_K || t > NM_LINEAR_MAX_ROWS || o > NM_LINEAR_MAX_ROWS) return NM_EUNSUPPORTED;
+  if (!some) return NM_OK;
+  nml::LinArgs a{};
+  a.x = static_cast<const uint16_t*>(x); a.w = static_cast<const uint16_t*>(w);
+  a.meta = static_cast<const uint8_t*>(w_meta);
+  a.ldx = ldx; a.ldw = ldw; a.t = t; a.o = o; a.k = k;
+  a.epi = nml::LinEpi{bias, residual, y, ldr, ldy, (int)fn, y_dtype == NM_Y_BF16};
+  a.route.flags = route;
+  a.route.taken = route_taken;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  float* part = static_cast<float*>(workspace);
+  const Kind kind = plan_linear(t, o, k, route);
+  if (kind == Kind::kFew || !nml::lin_tile_eligible(a)) return hip_status(nml::launch_lin_few(a, part, workspace_bytes, s));
+  return hip_status(nml::launch_lin_tile(a, kind == Kind::kLarge, part, workspace_bytes, s));
+}
+
+int64_t nm_linear_workspace_size(int64_t t, int64_t o, int64_t k, int sparse, uint32_t route) {
+  if (t <= 0 || o <= 0 || k <= 0 || k > NM_LINEAR_MAX_K || t > NM_LINEAR_MAX_ROWS || o > NM_LINEAR_MAX_ROWS) return 0;
+  const Kind kind = plan_linear(t, o, k, route);
+  if (kind == Kind::kLarge) return 0;
+  return kind == Kind::kFew ? nml::lin_few_part_bytes(t, o, k, sparse != 0) : nml::lin_mid_part_bytes(t, o, k);
+}
 
 nm_status nm_rmsnorm_i8(const void* x, nm_ydtype x_dtype, int64_t rows, int64_t k, int64_t ldx, const void* residual,
                         int64_t ldr, void* sum_out, int64_t lds, nm_ydtype stream_dtype, const float* weight, float eps,

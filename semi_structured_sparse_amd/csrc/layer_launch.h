@@ -34,6 +34,35 @@ struct RouteArgs {
 };
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s);
 
+// Output side of the bf16 products: y = residual + fn(sum + bias).
+struct LinEpi {
+  const float* bias;        // null: none
+  const void* residual;     // of y's type; null: none
+  void* y;
+  int64_t ldr, ldy;
+  int fn, bf16_out;
+};
+struct LinArgs {
+  const uint16_t* x;
+  const uint16_t* w;        // dense [o][ldw], or the kept values of 2:4 rows [o][ldw >= k / 2]
+  const uint8_t* meta;      // 2:4 positions [ceil(k/128)][o][16]; null: dense
+  int64_t ldx, ldw, t, o, k;
+  LinEpi epi;
+  Route route;
+};
+// Streaming kernel: any shape.  The reduction is split across workgroups where part holds
+// lin_few_part_bytes.
+hipError_t launch_lin_few(const LinArgs& a, float* part, int64_t part_bytes, hipStream_t s);
+int64_t lin_few_part_bytes(int64_t t, int64_t o, int64_t k, bool sparse);
+// Tile kernels: 256 x 256 tiles (large), or smaller ones by shape, the reduction split across
+// workgroups where part holds lin_mid_part_bytes.
+bool lin_tile_eligible(const LinArgs& a);
+int64_t lin_mid_part_bytes(int64_t t, int64_t o, int64_t k);
+hipError_t launch_lin_tile(const LinArgs& a, bool large, float* part, int64_t part_bytes, hipStream_t s);
+// y from `splits` partial sums part[split][t][o4], o4 = o rounded up to 4
+hipError_t launch_lin_reduce(const float* part, int64_t splits, int64_t t, int64_t o, const LinEpi& e, const Route& r,
+                             hipStream_t s);
+
 // The experts' MLPs of a few tokens.  Weights: row o of expert e at (e rows + o) ld bytes; 2:4
 // positions of an expert [ceil(k/128)][rows][16].
 struct MoeArgs {
