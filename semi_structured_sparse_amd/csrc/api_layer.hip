@@ -25,13 +25,18 @@ int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
 enum class Kind { kFew, kMid, kLarge };
 
-// Up to 32 tokens the streaming kernel, whose row blocks need no partial sums; above, 256 x 256
-// tiles where there are enough of them to fill the chip, smaller tiles below.
-Kind plan_linear(int64_t t, int64_t o, int64_t k, uint32_t route) {
+// Few tokens over short reductions: the streaming kernel, whose row blocks need no partial sums but
+// read X again each.  Otherwise 256 x 256 tiles where there are enough of them to fill the chip,
+// smaller tiles below.  Measured (us, streaming / smaller tiles, weights from HBM): 1 x 4096 x 4096
+// 10.5 / 11.8, 4 11.2 / 12.2, 8 11.9 / 12.2, 16 13.5 / 12.4, 32 17.5 / 13.4; 1 x 4096 x 14336 25.0 / 27.3, 4
+// 29.0 / 28.0, 16 37.9 / 29.1; 1 x 14336 x 4096 31.9 / 26.8; 8 x 256 x 2048 5.9 / 6.7, 32 9.0 / 7.0; 16 x
+// 4096 x 1024 6.5 / 6.4; 2:4 1 x 4096 x 4096 9.0 / 9.3, 4 9.7 / 9.6, 8 10.3 / 9.7; 1 x 4096 x 14336 22.0 /
+// 21.9; 1 x 14336 x 4096 22.1 / 18.9; 8 x 256 x 2048 5.7 / 6.6.
+Kind plan_linear(int64_t t, int64_t o, int64_t k, bool sparse, uint32_t route) {
   if (route & NM_ROUTE_FEW_STREAM) return Kind::kFew;
   if (route & NM_ROUTE_FEW_TILE) return Kind::kMid;
   if (route & NM_ROUTE_TILE_LDS) return Kind::kLarge;
-  if (t <= 32) return (o + 63) / 64 >= 192 || (t > 8 && t * k > 8 * 8192) ? Kind::kMid : Kind::kFew;
+  if (t <= 16 && o < 8192 && t * k <= (sparse ? 16384 : 32768)) return Kind::kFew;
   return ((o + 255) / 256) * ((t + 255) / 256) >= 160 ? Kind::kLarge : Kind::kMid;
 }
 
@@ -64,16 +69,16 @@ nm_status nm_linear(const void* x, int64_t t, int64_t k, int64_t ldx, const void
   a.route.taken = route_taken;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   float* part = static_cast<float*>(workspace);
-  const Kind kind = plan_linear(t, o, k, route);
+  const Kind kind = plan_linear(t, o, k, sp, route);
   if (kind == Kind::kFew || !nml::lin_tile_eligible(a)) return hip_status(nml::launch_lin_few(a, part, workspace_bytes, s));
   return hip_status(nml::launch_lin_tile(a, kind == Kind::kLarge, part, workspace_bytes, s));
 }
 
 int64_t nm_linear_workspace_size(int64_t t, int64_t o, int64_t k, int sparse, uint32_t route) {
   if (t <= 0 || o <= 0 || k <= 0 || k > NM_LINEAR_MAX_K || t > NM_LINEAR_MAX_ROWS || o > NM_LINEAR_MAX_ROWS) return 0;
-  const Kind kind = plan_linear(t, o, k, route);
+  const Kind kind = plan_linear(t, o, k, sparse != 0, route);
   if (kind == Kind::kLarge) return 0;
-  return kind == Kind::kFew ? nml::lin_few_part_bytes(t, o, k, sparse != 0) : nml::lin_mid_part_bytes(t, o, k);
+  return kind == Kind::kFew ? nml::lin_few_part_bytes(t, o, k, sparse != 0) : nml::lin_mid_part_bytes(t, o, k, sparse != 0);
 }
 
 nm_status nm_rmsnorm_i8(const void* x, nm_ydtype x_dtype, int64_t rows, int64_t k, int64_t ldx, const void* residual,

@@ -57,7 +57,7 @@ int64_t lin_few_part_bytes(int64_t t, int64_t o, int64_t k, bool sparse);
 // Tile kernels: 256 x 256 tiles (large), or smaller ones by shape, the reduction split across
 // workgroups where part holds lin_mid_part_bytes.
 bool lin_tile_eligible(const LinArgs& a);
-int64_t lin_mid_part_bytes(int64_t t, int64_t o, int64_t k);
+int64_t lin_mid_part_bytes(int64_t t, int64_t o, int64_t k, bool sparse);
 hipError_t launch_lin_tile(const LinArgs& a, bool large, float* part, int64_t part_bytes, hipStream_t s);
 // y from `splits` partial sums part[split][t][o4], o4 = o rounded up to 4
 hipError_t launch_lin_reduce(const float* part, int64_t splits, int64_t t, int64_t o, const LinEpi& e, const Route& r,

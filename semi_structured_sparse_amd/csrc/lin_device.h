@@ -52,8 +52,9 @@ __device__ __forceinline__ void lin_fns(float (&v)[N], int fn) {
 }
 
 // Four neighbouring outputs of a row, on a multiple of their size: the residual's, as loaded ...
+template <bool BF16>
 __device__ __forceinline__ uint4 lin_load4(const nml::LinEpi& e, int64_t t, int64_t o) {
-  if (e.bf16_out) {
+  if constexpr (BF16) {
     const uint2 d = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.residual) + t * e.ldr + o);
     return make_uint4(d.x, d.y, 0u, 0u);
   }

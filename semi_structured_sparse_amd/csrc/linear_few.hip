@@ -211,7 +211,8 @@ __global__ __launch_bounds__(256) void k_lin_reduce(const float* __restrict__ pa
     }
   }
   if (whole) {
-    const uint4 r = epi.residual != nullptr ? lin_load4(epi, t, o) : make_uint4(0u, 0u, 0u, 0u);
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if (epi.residual != nullptr) r = epi.bf16_out ? lin_load4<true>(epi, t, o) : lin_load4<false>(epi, t, o);
     float v[4] = {s[0], s[1], s[2], s[3]};
     if (epi.bias != nullptr) {
       const f32x4 b = *reinterpret_cast<const f32x4*>(epi.bias + o);
@@ -232,6 +233,13 @@ struct FewPlan {
   int64_t splits;
 };
 
+// Row blocks of a workgroup: every workgroup reads all of X again, so as many as leave 200
+// workgroups.  Waves: four where there are 192 workgroups, whose two batches each keep enough loads
+// in flight (1 x 4096 x 4096 with 4 / 8 / 16 waves: 10.2 / 10.1 / 10.6 us, 2:4 8.1 / 8.6 / 9.2, 4 x 4096
+// x 14336 28.6 / 30.3 / 29.1).  Below, eight, and the reduction split up to one workgroup per CU,
+// four steps a wave at least, if a wave has over eight unsplit (1 x 1024 x 4096: 16 waves unsplit
+// 8.4 us, 16 in two ranges 8.2, 8 in four 7.7); sixteen where that leaves one range (1 x 256 x 2048:
+// 5.2).
 FewPlan few_plan(int64_t t, int64_t o, int64_t k, bool sparse) {
   FewPlan p;
   p.tb = t <= 16 ? 1 : t <= 32 ? 2 : 4;
@@ -240,15 +248,13 @@ FewPlan few_plan(int64_t t, int64_t o, int64_t k, bool sparse) {
   p.rw = p.tb > 2 ? 1 : p.tb == 2 ? 2 : 4;
   while (p.rw > 1 && ((o + 16 * p.rw - 1) / (16 * p.rw)) * gy < 200) p.rw /= 2;
   const int64_t blocks = ((o + 16 * p.rw - 1) / (16 * p.rw)) * gy;
-  p.waves = blocks <= 256 ? 16 : blocks <= 512 ? 8 : 4;
-  const int most = p.tb == 4 || p.rw * p.tb > 4 ? 8 : 16;   // 64 KiB of partial tiles
-  if (p.waves > most) p.waves = most;
-  while (p.waves > 4 && steps < 2 * p.waves) p.waves /= 2;
+  p.waves = blocks >= 192 ? 4 : 8;
   int64_t s = blocks > 0 ? 256 / blocks : 1;
   const int64_t room = steps / (4 * p.waves);
   if (s > room) s = room;
   if (steps <= 8 * p.waves) s = 1;
   p.splits = s < 2 ? 1 : s > 16 ? 16 : s;
+  if (blocks <= 32 && p.splits == 1 && p.tb < 4 && steps >= 32) p.waves = 16;   // 64 KiB of partial tiles
   return p;
 }
 
