@@ -155,7 +155,7 @@ nm_status nm_moe_i8(const nm_moe_args* args, void* stream) {
   if (g.hidden > NM_I8_MAX_K || g.inter > 65536 || g.experts > NM_MOE_MAX_EXPERTS || g.top > NM_MOE_MAX_TOP)
     return NM_EUNSUPPORTED;
   if (!some) return NM_OK;
-  if (g.workspace == nullptr || g.workspace_bytes < nml::moe_workspace_bytes(g.t, g.top, g.inter)) return NM_EINVAL;
+  if (g.workspace == nullptr || g.workspace_bytes < nml::moe_workspace_bytes(g.t, g.experts, g.top, g.hidden, g.inter)) return NM_EINVAL;
   nml::MoeArgs a{};
   a.x = g.x; a.x_scale = g.x_scale; a.ids = g.ids; a.weights = g.weights;
   a.w_gate = g.w_gate; a.w_up = g.w_up; a.w_down = g.w_down;
@@ -174,7 +174,7 @@ int64_t nm_moe_i8_workspace_size(int64_t t, int64_t experts, int64_t top, int64_
   (void)sparse;
   if (t <= 0 || experts <= 0 || top <= 0 || hidden <= 0 || inter < 0) return 0;
   if (hidden > NM_I8_MAX_K || inter > 65536 || experts > NM_MOE_MAX_EXPERTS || top > NM_MOE_MAX_TOP) return 0;
-  return nml::moe_workspace_bytes(t, top, inter);
+  return nml::moe_workspace_bytes(t, experts, top, hidden, inter);
 }
 
 }  // extern "C"

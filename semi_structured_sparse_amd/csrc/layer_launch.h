@@ -79,7 +79,7 @@ struct MoeArgs {
   int64_t t, hidden, inter;
   int experts, top, act, bf16_out;
 };
-int64_t moe_workspace_bytes(int64_t t, int64_t top, int64_t inter);
+int64_t moe_workspace_bytes(int64_t t, int64_t experts, int64_t top, int64_t hidden, int64_t inter);
 hipError_t launch_moe_i8(const MoeArgs& a, void* ws, hipStream_t s);
 
 }  // namespace nml

@@ -22,7 +22,8 @@ namespace {
 using namespace nmk;
 using namespace nml;
 
-constexpr int kPass = 64;   // tokens of a pass: bits of a mask
+constexpr int kPass = 64;      // tokens of a pass: bits of a mask
+constexpr int kMaxParts = 8;   // of the down products' item sequence
 
 struct Item {
   int expert, base, count;  // slots [base, base + count): the item's tokens in ascending order
@@ -38,6 +39,7 @@ struct Plan {
   uint16_t* h;              // bf16 [slots][ldh]
   int8_t* hq;               // [slots][ldh]
   float* hs;                // [slots]
+  float* part;              // [parts][t][hidden], if the down products are cut
   int64_t ldh;
 };
 
@@ -105,16 +107,23 @@ __device__ __forceinline__ uint32_t before_lane(const unsigned long long* mask, 
   return sum - own;
 }
 
-// Gate and up of an item's tokens for 16 hidden units: blockIdx.x the units, blockIdx.y the item.
+// Gate and up of an item's tokens (blockIdx.y the item) for 16 hidden units.  The waves share the
+// reduction in contiguous parts, so that a workgroup reads whole rows.  Many short workgroups: what
+// one waits for, its plan, its first weights, its sum, lies behind the others' weights.  (Two or
+// four blocks of units a workgroup, their batches one sequence: 64 tokens 6/64 4096 x 1408 235 and 244
+// us a layer instead of 221; a block a wave instead of a workgroup 237, and 1 token 2/8 4096 x
+// 14336 80 instead of 73.)  Batches of four steps, two of 2:4 weights, whose registers leave room for
+// twice the workgroups (8 tokens 8/64 2048 x 1024 50 us, with four 57).
 template <int TB, bool SP>
-__global__ __launch_bounds__(512) void k_moe_glu(MoeArgs a, Plan p, int t) {
-  constexpr int NA = 2, STEP = SP ? 128 : 64;
-  constexpr int U = TB == 1 ? 4 : TB == 2 ? 3 : 2;
-  extern __shared__ __align__(16) unsigned char lds[];   // masks, then [waves][NA][16 TB][16] sums
+__global__ __launch_bounds__(256) void k_moe_glu(MoeArgs a, Plan p, int t) {
+  constexpr int NA = 2, STEP = SP ? 128 : 64, NW = 4;
+  constexpr int U = TB == 1 ? (SP ? 2 : 4) : 2;
+  constexpr int TILE = NA * TB * 256;
+  __shared__ __align__(16) int red[NW * TILE];           // [waves][NA][16 TB][16] sums
+  extern __shared__ __align__(16) unsigned char lds[];   // masks
   unsigned long long* const mask = reinterpret_cast<unsigned long long*>(lds);
-  int* const red = reinterpret_cast<int*>(lds + (a.experts * 8 + 15) / 16 * 16);
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fq = lane >> 4;
   expert_masks(mask, a.ids, t, a.top, a.experts);
   const int per = (a.experts + 63) / 64;
@@ -169,20 +178,22 @@ __global__ __launch_bounds__(512) void k_moe_glu(MoeArgs a, Plan p, int t) {
   const int64_t O = a.inter;
   const int k = (int)a.hidden, wlen = SP ? k / 2 : k;
   const int8_t* xrow[TB];
+  float xs[TB];   // of the thread's outputs: token 16 j + tid / 16, hidden unit tid % 16
 #pragma unroll
   for (int j = 0; j < TB; ++j) {
-    const int r = 16 * TB * blk + min(16 * j + fr, count - 1);
-    xrow[j] = a.x + (int64_t)__shfl(token, r, 64) * a.ldx + 16 * fq;
+    xrow[j] = a.x + (int64_t)__shfl(token, 16 * TB * blk + min(16 * j + fr, count - 1), 64) * a.ldx + 16 * fq;
+    xs[j] = a.x_scale[__shfl(token, 16 * TB * blk + min(16 * j + (int)(threadIdx.x >> 4), count - 1), 64)];
   }
-  const int64_t ob = (int64_t)blockIdx.x * 16;
-  const int64_t o_l = ob + fr < O ? ob + fr : O - 1;
   const int64_t msteps = (k + 127) / 128;
+  const int64_t ob = (int64_t)blockIdx.x * 16;
+  const int64_t o_l = min(ob + fr, O - 1), o_t = min(ob + (threadIdx.x & 15), O - 1);
+  const float gs = a.gate_scale[e * O + o_t], us = a.up_scale[e * O + o_t];   // of the thread's outputs
   const int8_t* wrow[NA] = {a.w_gate + (e * O + o_l) * a.ldw + 16 * fq, a.w_up + (e * O + o_l) * a.ldw + 16 * fq};
   const int64_t mat = (e * msteps * O + o_l) * 16 + 4 * fq;
   const uint8_t* mrow[NA] = {SP ? a.gate_meta + mat : nullptr, SP ? a.up_meta + mat : nullptr};
 
   const int steps = (k + STEP - 1) / STEP;
-  const int s0 = wave * steps / waves, s1 = (wave + 1) * steps / waves;
+  const int s0 = wave * steps / NW, s1 = (wave + 1) * steps / NW;
   i32x4 acc[NA][TB];
 #pragma unroll
   for (int i = 0; i < NA; ++i)
@@ -219,39 +230,44 @@ __global__ __launch_bounds__(512) void k_moe_glu(MoeArgs a, Plan p, int t) {
       multiply<U, NA, TB, SP>(acc, b1);
     }
   }
-
-  // the waves' partial tiles: red[wave][a][token][unit]
-  constexpr int TILE = NA * TB * 256;
+  // the waves' partial tiles: red[wave][matrix][token][unit]
 #pragma unroll
   for (int i = 0; i < NA; ++i)
 #pragma unroll
     for (int j = 0; j < TB; ++j)
       *reinterpret_cast<i32x4*>(red + wave * TILE + ((i * TB + j) * 16 + fr) * 16 + 4 * fq) = acc[i][j];
-  // tokens of the item by rank, for the threads of the sums
-  __shared__ int item_tok[16 * TB];
-  {
-    const int tok = __shfl(token, 16 * TB * blk + min(lane, count - 1), 64);
-    if (wave == 0 && lane < 16 * TB) item_tok[lane] = tok;
-  }
   __syncthreads();
-  for (int i = threadIdx.x; i < count * 16; i += blockDim.x) {
-    const int r = i & 15, tl = i >> 4;
-    const int64_t o = ob + r;
-    if (o >= O) continue;
+  const int64_t o = ob + (threadIdx.x & 15);
+#pragma unroll
+  for (int j = 0; j < TB; ++j) {
+    const int tl = 16 * j + (int)(threadIdx.x >> 4);
+    if (tl >= count || o >= O) continue;
     int v0 = 0, v1 = 0;
-    for (int wv = 0; wv < waves; ++wv) {
-      v0 += red[wv * TILE + tl * 16 + r];
-      v1 += red[wv * TILE + TB * 256 + tl * 16 + r];
+#pragma unroll
+    for (int wv = 0; wv < NW; ++wv) {
+      v0 += red[wv * TILE + tl * 16 + (threadIdx.x & 15)];
+      v1 += red[wv * TILE + TB * 256 + tl * 16 + (threadIdx.x & 15)];
     }
-    const float xs = a.x_scale[item_tok[tl]];
-    const float h = glu_gate(i8_scaled(v0, xs, a.gate_scale[e * O + o]), a.act) * i8_scaled(v1, xs, a.up_scale[e * O + o]);
+    const float h = glu_gate(i8_scaled(v0, xs[j], gs), a.act) * i8_scaled(v1, xs[j], us);
     p.h[(int64_t)(base + tl) * p.ldh + o] = bf16_rne(h);
   }
 }
 
+__device__ __forceinline__ void moe_store(const MoeArgs& a, float v, int64_t tok, int64_t o) {
+  if (a.bf16_out) {
+    if (a.residual != nullptr)
+      v += __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.residual)[tok * a.ldr + o] << 16);
+    static_cast<uint16_t*>(a.y)[tok * a.ldy + o] = bf16_rne(v);
+  } else {
+    if (a.residual != nullptr) v += static_cast<const float*>(a.residual)[tok * a.ldr + o];
+    static_cast<float*>(a.y)[tok * a.ldy + o] = v;
+  }
+}
+
 // Down products of every item for 16 outputs, each token's summed with its weights.  The items'
-// steps are one sequence of batches that the waves share in contiguous parts; a wave adds what
-// it has of an item to its own sums in LDS, and the waves' sums are added in their order.
+// steps are one sequence of batches that the waves (of all blockIdx.y, where there are too few
+// blocks of outputs to fill the chip) share in contiguous parts; a wave adds what it has of an
+// item to its own sums in LDS, and the waves' sums are added in their order.
 template <int TB, bool SP>
 __global__ __launch_bounds__(512) void k_moe_down(MoeArgs a, Plan p, int t) {
   constexpr int STEP = SP ? 128 : 64;
@@ -271,7 +287,8 @@ __global__ __launch_bounds__(512) void k_moe_down(MoeArgs a, Plan p, int t) {
   const int64_t o_l = ob + fr < O ? ob + fr : O - 1;
   const int64_t msteps = (k + 127) / 128;
   const int steps = (k + STEP - 1) / STEP, nbat = (steps + U - 1) / U;
-  const int g0 = (int)((int64_t)wave * items * nbat / waves), g1 = (int)((int64_t)(wave + 1) * items * nbat / waves);
+  const int parts = waves * (int)gridDim.y, part = (int)blockIdx.y * waves + wave;
+  const int g0 = (int)((int64_t)part * items * nbat / parts), g1 = (int)((int64_t)(part + 1) * items * nbat / parts);
 
   struct Work {                // a batch, and what its item's sums are scaled with
     Batch<U, 1, TB, SP> b;
@@ -363,22 +380,41 @@ __global__ __launch_bounds__(512) void k_moe_down(MoeArgs a, Plan p, int t) {
     if (o >= O) continue;
     float v = 0.0f;
     for (int wv = 0; wv < waves; ++wv) v += sums[wv * t * 16 + i];
-    if (a.bf16_out) {
-      if (a.residual != nullptr)
-        v += __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.residual)[tok * a.ldr + o] << 16);
-      static_cast<uint16_t*>(a.y)[tok * a.ldy + o] = bf16_rne(v);
-    } else {
-      if (a.residual != nullptr) v += static_cast<const float*>(a.residual)[tok * a.ldr + o];
-      static_cast<float*>(a.y)[tok * a.ldy + o] = v;
-    }
+    if (gridDim.y > 1) p.part[((int64_t)blockIdx.y * t + tok) * O + o] = v;
+    else moe_store(a, v, tok, o);
   }
+}
+
+// y from the parts of blockIdx.y, part[part][t][hidden], in their order.
+__global__ __launch_bounds__(256) void k_moe_sum(MoeArgs a, const float* __restrict__ part, int parts, int t) {
+  const int64_t n = (int64_t)t * a.hidden;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float v[kMaxParts];
+#pragma unroll
+  for (int e = 0; e < kMaxParts; ++e) v[e] = part[(e < parts ? e : 0) * n + i];
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kMaxParts; ++e) s += e < parts ? v[e] : 0.0f;
+  const int64_t tok = i / a.hidden;
+  moe_store(a, s, tok, i - tok * a.hidden);
 }
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
+// Parts that the down products' item sequence is cut in.
+int down_parts(int64_t t, int64_t experts, int64_t top, int64_t hidden, int64_t inter) {
+  const int64_t blocks = (hidden + 15) / 16, slots = t * top, asked = slots < experts ? slots : experts;
+  int64_t parts = blocks > 0 ? 256 / blocks : 1;
+  const int64_t room = asked * ((inter + 63) / 64) / 64;   // steps: eight waves, eight each
+  if (parts > room) parts = room;
+  return parts < 2 ? 1 : parts > kMaxParts ? kMaxParts : (int)parts;
+}
+
 // Places in the workspace, and its size, for passes of up to kPass tokens.
-int64_t lay_out(Plan& p, unsigned char* ws, int64_t t, int64_t top, int64_t inter) {
-  const int64_t slots = (t < kPass ? t : kPass) * top;
+int64_t lay_out(Plan& p, unsigned char* ws, int64_t t, int64_t experts, int64_t top, int64_t hidden, int64_t inter) {
+  if (t > kPass) t = kPass;
+  const int64_t slots = t * top;
   p.ldh = up16(inter);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -393,6 +429,8 @@ int64_t lay_out(Plan& p, unsigned char* ws, int64_t t, int64_t top, int64_t inte
   p.hs = reinterpret_cast<float*>(take(slots * 4));
   p.hq = reinterpret_cast<int8_t*>(take(slots * p.ldh));
   p.h = reinterpret_cast<uint16_t*>(take(slots * p.ldh * 2));
+  const int parts = down_parts(t, experts, top, hidden, inter);
+  p.part = reinterpret_cast<float*>(take(parts > 1 ? parts * t * hidden * 4 : 0));
   return at;
 }
 
@@ -403,16 +441,18 @@ hipError_t launch_pass(const MoeArgs& a, const Plan& p, int t, hipStream_t s) {
   const int items = slots < asked + slots / (16 * TB) ? slots : asked + slots / (16 * TB);
   const int64_t nob = (a.inter + 15) / 16, nod = (a.hidden + 15) / 16;
   if (nob > 0x7FFFFF || nod > 0x7FFFFF) return hipErrorInvalidConfiguration;
-  const int waves = 4;
-  const size_t lds = (size_t)(a.experts * 8 + 15) / 16 * 16 + (size_t)waves * 2 * TB * 1024;
   if (a.inter > 0) {   // otherwise no batch of the down products exists, whatever the plan holds
-    k_moe_glu<TB, SP><<<dim3((unsigned)nob, (unsigned)items), dim3(64 * waves), lds, s>>>(a, p, t);
+    k_moe_glu<TB, SP><<<dim3((unsigned)nob, (unsigned)items), dim3(256), (size_t)(a.experts * 8 + 15) / 16 * 16, s>>>(a, p, t);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     e = launch_quant_i8(p.h, slots, a.inter, p.ldh, 0, 0, 2, p.hq, p.ldh, p.hs, s);
     if (e != hipSuccess) return e;
   }
-  k_moe_down<TB, SP><<<dim3((unsigned)nod), dim3(512), (size_t)8 * t * 64, s>>>(a, p, t);
+  const int parts = down_parts(t, a.experts, a.top, a.hidden, a.inter);
+  k_moe_down<TB, SP><<<dim3((unsigned)nod, (unsigned)parts), dim3(512), (size_t)8 * t * 64, s>>>(a, p, t);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || parts == 1) return e;
+  k_moe_sum<<<dim3((unsigned)(((int64_t)t * a.hidden + 255) / 256)), dim3(256), 0, s>>>(a, p.part, parts, t);
   return hipGetLastError();
 }
 
@@ -420,18 +460,21 @@ hipError_t launch_pass(const MoeArgs& a, const Plan& p, int t, hipStream_t s) {
 
 namespace nml {
 
-int64_t moe_workspace_bytes(int64_t t, int64_t top, int64_t inter) {
+int64_t moe_workspace_bytes(int64_t t, int64_t experts, int64_t top, int64_t hidden, int64_t inter) {
   Plan p;
-  return lay_out(p, nullptr, t, top, inter);
+  int64_t most = lay_out(p, nullptr, t, experts, top, hidden, inter);
+  const int64_t rest = t > kPass ? t % kPass : 0;
+  const int64_t last = rest > 0 ? lay_out(p, nullptr, rest, experts, top, hidden, inter) : 0;
+  return most > last ? most : last;
 }
 
 hipError_t launch_moe_i8(const MoeArgs& a, void* ws, hipStream_t s) {
-  Plan p;
-  lay_out(p, static_cast<unsigned char*>(ws), a.t, a.top, a.inter);
   for (int64_t t0 = 0; t0 < a.t; t0 += kPass) {
     MoeArgs b = a;
     const int t = (int)(a.t - t0 < kPass ? a.t - t0 : kPass);
     const int64_t size = a.bf16_out ? 2 : 4;
+    Plan p;
+    lay_out(p, static_cast<unsigned char*>(ws), t, a.experts, a.top, a.hidden, a.inter);
     b.t = t;
     b.x = a.x + t0 * a.ldx;
     b.x_scale = a.x_scale + t0;
