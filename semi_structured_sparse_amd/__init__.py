@@ -230,13 +230,13 @@ _current_raw_stream = None      # device -> raw current stream
 _current_device = None          # () -> the current device
 # element types of the int8 layers: codes, rows of bf16 (or their bits), and fp16, which y must not be
 _int8s = _bf16s = _half = None
-_f32s = _int32s = None          # of the operators around the products
+_f32 = _bf16 = _int32 = None    # of the operators around the products
 
 
 def _bind_types(torch):
-    global _int8s, _bf16s, _half, _f32s, _int32s
+    global _int8s, _bf16s, _half, _f32, _bf16, _int32
     _int8s, _bf16s, _half = (torch.int8, torch.uint8), (torch.bfloat16, torch.int16, torch.uint16), torch.float16
-    _f32s, _int32s = (torch.float32,), (torch.int32,)
+    _f32, _bf16, _int32 = torch.float32, torch.bfloat16, torch.int32
 
 
 def _bind_torch():
@@ -772,24 +772,24 @@ def _rows_of(t, dev, rows, cols, whole, ld, kind, name):
     type of raw pointers (None: fp32), which a tensor has to agree with."""
     if t is None or type(t) is int:
         return t, ld or 0, NM_Y_F32 if kind is None else kind
-    st = t.stride()
-    have = NM_Y_F32 if t.dtype in _f32s else NM_Y_BF16 if t.dtype in _bf16s else -1
+    st, d = t.stride(), t.dtype
+    have = NM_Y_BF16 if d is _bf16 else NM_Y_F32 if d is _f32 else NM_Y_BF16 if d in _bf16s else -1
     if len(st) != 2 or st[1] != 1 or t.get_device() != dev or have < 0 or (kind is not None and kind != have):
         _refuse(t, dev, f"{name}: a matrix with contiguous rows of fp32 or bf16 values is needed")
-    sh = t.shape
+    r, c = t.shape
     if ld is None:
         ld = st[0] if cols else 0       # of no columns: torch has 1
-    if sh[0] < rows or sh[1] < cols + -cols % whole or ld != st[0]:
+    if r < rows or c < cols or c & (whole - 1) or ld != st[0]:
         _holds(t, rows, cols, whole, ld)
     return t.data_ptr(), ld, have
 
 
-def _list_of(t, n, dev, types, name):
-    """Pointer of at least n contiguous values of one of the types (None -> NULL, integers are raw
+def _list_of(t, n, dev, kind, name):
+    """Pointer of at least n contiguous values of 4 bytes of a type (None -> NULL, integers are raw
     pointers)."""
     if t is None or type(t) is int:
         return t
-    if t.get_device() != dev or t.dtype not in types or t.numel() < n or not t.is_contiguous():
+    if t.get_device() != dev or t.dtype is not kind or t.nbytes < 4 * n or not t.is_contiguous():
         _refuse(t, dev, f"{name}: {n} contiguous values are needed")
     return t.data_ptr()
 
@@ -830,7 +830,7 @@ def nm_linear(x, w, y, w_meta=None, bias=None, fn=NM_FN_NONE, residual=None, wor
     rp, lr = (None, 0) if residual is None else _rows_of(residual, dev, t, o, 1, ldr, yd, "residual")[:2]
     wsp, wsn = _scratch(workspace, workspace_bytes, dev)
     res = lib().nm_linear(xp, t, k, lx, wp, o, lw, _meta(w_meta, o, k, dev),
-                          None if bias is None else _list_of(bias, o, dev, _f32s, "bias"), fn, rp, lr, yp, ly, yd, wsp, wsn,
+                          None if bias is None else _list_of(bias, o, dev, _f32, "bias"), fn, rp, lr, yp, ly, yd, wsp, wsn,
                           route, ctypes.addressof(taken) if taken is not None else None, stream)
     if check and res:
         _check(res, "nm_linear")
@@ -856,8 +856,14 @@ def nm_rmsnorm_i8(x, weight, q, scale, residual=None, sum_out=None, y=None, eps=
         k = x.shape[1]
     xp, lx, xt = _rows_of(x, dev, rows, k, 8, ldx, x_dtype, "x")
     rp, lr, rt = _rows_of(residual, dev, rows, k, 8, ldr, stream_dtype, "residual")
-    sp, ls, st = _rows_of(sum_out, dev, rows, k, 1, lds, rt if residual is not None else stream_dtype, "sum_out")
-    yp, ly, _ = _rows_of(y, dev, rows, k, 1, ldy, NM_Y_BF16, "y")
+    sp = yp = None
+    ls = ly = 0
+    if sum_out is not None:
+        sp, ls, st = _rows_of(sum_out, dev, rows, k, 1, lds, rt if residual is not None else stream_dtype, "sum_out")
+        if residual is None:
+            rt = st
+    if y is not None:
+        yp, ly, _ = _rows_of(y, dev, rows, k, 1, ldy, NM_Y_BF16, "y")
     qp, lq = _mat(q, dev, _int8s, "int8 codes")
     if ldq is not None:
         lq = ldq
@@ -870,9 +876,9 @@ def nm_rmsnorm_i8(x, weight, q, scale, residual=None, sum_out=None, y=None, eps=
             _holds(q, rows, kq, 16, lq)
     if k == 0:
         lq = ldq or 0
-    res = lib().nm_rmsnorm_i8(xp, xt, rows, k, lx, rp, lr, sp, ls, rt if residual is not None else st,
-                              _list_of(weight, k, dev, _f32s, "weight"), eps, n, m, ns, yp, ly, qp, lq,
-                              _list_of(scale, rows, dev, _f32s, "scale"), stream)
+    res = lib().nm_rmsnorm_i8(xp, xt, rows, k, lx, rp, lr, sp, ls, rt,
+                              _list_of(weight, k, dev, _f32, "weight"), eps, n, m, ns, yp, ly, qp, lq,
+                              _list_of(scale, rows, dev, _f32, "scale"), stream)
     if check and res:
         _check(res, "nm_rmsnorm_i8")
     return res
@@ -893,9 +899,9 @@ def nm_moe_route(logits, ids, weights, kind=NM_ROUTER_SOFTMAX, bias=None, renorm
     if top is None:
         top = ids.shape[1]
     lp, ll, _ = _rows_of(logits, dev, t, experts, 1, ldl, NM_Y_F32, "logits")
-    res = lib().nm_moe_route(lp, t, experts, ll, _list_of(bias, experts, dev, _f32s, "bias"), kind, top,
-                             1 if renormalize else 0, scale, _list_of(ids, t * top, dev, _int32s, "ids"),
-                             _list_of(weights, t * top, dev, _f32s, "weights"), stream)
+    res = lib().nm_moe_route(lp, t, experts, ll, _list_of(bias, experts, dev, _f32, "bias"), kind, top,
+                             1 if renormalize else 0, scale, _list_of(ids, t * top, dev, _int32, "ids"),
+                             _list_of(weights, t * top, dev, _f32, "weights"), stream)
     if check and res:
         _check(res, "nm_moe_route")
     return res
@@ -953,17 +959,17 @@ def nm_moe_i8(x, x_scale, ids, weights, w_gate, gate_scale, w_up, up_scale, w_do
     a = nm_moe_args()
     a.t, a.hidden, a.inter, a.experts, a.top, a.act = t, hidden, inter, experts, top, act
     a.x, a.ldx = _codes(x, None if x is None or type(x) is int else x.shape, dev, t, hidden, ldx)
-    a.x_scale = _list_of(x_scale, t, dev, _f32s, "x_scale")
-    a.ids = _list_of(ids, t * top, dev, _int32s, "ids")
-    a.weights = _list_of(weights, t * top, dev, _f32s, "weights")
+    a.x_scale = _list_of(x_scale, t, dev, _f32, "x_scale")
+    a.ids = _list_of(ids, t * top, dev, _int32, "ids")
+    a.weights = _list_of(weights, t * top, dev, _f32, "weights")
     a.w_gate, a.ldw = _expert_codes(w_gate, dev, experts, inter, wk, ldw, "w_gate")
     a.w_up, lu = _expert_codes(w_up, dev, experts, inter, wk, ldw, "w_up")
     if lu != a.ldw:
         raise ValueError("w_gate and w_up need the same leading dimension")
     a.w_down, a.ldd = _expert_codes(w_down, dev, experts, hidden, dk, ldd, "w_down")
-    a.gate_scale = _list_of(gate_scale, experts * inter, dev, _f32s, "gate_scale")
-    a.up_scale = _list_of(up_scale, experts * inter, dev, _f32s, "up_scale")
-    a.down_scale = _list_of(down_scale, experts * hidden, dev, _f32s, "down_scale")
+    a.gate_scale = _list_of(gate_scale, experts * inter, dev, _f32, "gate_scale")
+    a.up_scale = _list_of(up_scale, experts * inter, dev, _f32, "up_scale")
+    a.down_scale = _list_of(down_scale, experts * hidden, dev, _f32, "down_scale")
     a.gate_meta = _meta(gate_meta, experts * inter, hidden, dev)
     a.up_meta = _meta(up_meta, experts * inter, hidden, dev)
     a.down_meta = _meta(down_meta, experts * hidden, inter, dev)

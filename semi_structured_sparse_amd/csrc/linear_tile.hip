@@ -434,7 +434,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_lin_tile(
 #pragma unroll
     for (int c = 0; c < KM; ++c) {
       const int ch = s * KM + c;   // past the last chunk: zeros
-      const uint32_t at = ch < chunks - 1 ? 0u : ch == chunks - 1 ? atail : kPast;
+      const uint32_t at = ch == chunks - 1 ? atail : KM > 1 && ch >= chunks ? kPast : 0u;
 #pragma unroll
       for (int q = 0; q < NA; ++q)
         b2lds16(rw, a + c * A_CHUNK + (wave + q * NW) * 1024, aoff[q] | at, (uint32_t)(ch * AROW));
@@ -447,7 +447,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_lin_tile(
 #pragma unroll
     for (int c = 0; c < KM; ++c) {
       const int ch = s * KM + c;
-      const uint32_t bt = ch < chunks - 1 ? 0u : ch == chunks - 1 ? btail : kPast;
+      const uint32_t bt = ch == chunks - 1 ? btail : KM > 1 && ch >= chunks ? kPast : 0u;
 #pragma unroll
       for (int q = 0; q < NB; ++q)
         b2lds16(rx, b + c * B_CHUNK + (wave + q * NW) * 1024, boff[q] | bt, (uint32_t)(ch * 128));

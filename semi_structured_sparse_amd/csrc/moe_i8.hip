@@ -271,7 +271,7 @@ __device__ __forceinline__ void moe_store(const MoeArgs& a, float v, int64_t tok
 template <int TB, bool SP>
 __global__ __launch_bounds__(512) void k_moe_down(MoeArgs a, Plan p, int t) {
   constexpr int STEP = SP ? 128 : 64;
-  constexpr int U = TB == 1 ? (SP ? 4 : 6) : TB == 2 ? 3 : 2;
+  constexpr int U = SP && TB == 1 ? 4 : 2;
   extern __shared__ __align__(16) unsigned char lds[];   // [waves][t][16] sums
   float* const sums = reinterpret_cast<float*>(lds);
   const int lane = threadIdx.x & 63;
