@@ -10,7 +10,13 @@
 // order like them, 0 for an expert that cannot be chosen (a logit of -inf or NaN).  A round finds
 // the largest key of the wave by cross-lane moves (no LDS), the first lane that holds it by a
 // ballot, and takes that expert out: the lowest index of equals, since a lane's own best is its
-// first.
+// first.  What is recorded is the expert's number; its logit is read again from the row, which is in
+// the cache by then: chosen by a uniform index from the lane's values, the compiler moves those into
+// LDS (8192 x 256, 8 of biased scores: 24.8 us instead of 11.3).
+//
+// Bound by the rounds' chains of dependent cross-lane moves, not by memory: 8192 tokens, 8 chosen,
+// 64 / 256 / 512 biased experts 6.5 / 11.3 / 21.3 us, 256 by softmax 7.8 (8.9 MB: 1.5 at the rate of
+// a large copy); 16 x 64 3.2 us, most of it the launch.
 #include <type_traits>
 
 #include "layer_launch.h"
@@ -66,32 +72,15 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// NV: experts a lane; BIASED: the choice by biased sigmoid scores
-template <int NV, bool BIASED>
-__global__ __launch_bounds__(256) void k_moe_route(RouteArgs a) {
-  using Key = typename std::conditional<BIASED, uint64_t, uint32_t>::type;
+// The value of a key.
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k); }
+
+// Up to n rounds: won(j, key, lane, which) is told the j-th largest key and where it lies, the lowest
+// expert of equals, and says whether to go on.
+template <int NV, typename Key, typename Won>
+__device__ __forceinline__ void rounds(Key (&key)[NV], int n, Won&& won) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= a.t) return;   // whole waves, and no barrier below
-  const float* row = a.logits + t * a.ldl;
-  const int e0 = lane * NV, E = (int)a.experts;
-  float l[NV];
-  Key key[NV];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) l[v] = e0 + v < E ? row[e0 + v] : -__builtin_inff();
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const bool open = l[v] > -__builtin_inff();   // false for NaN
-    if constexpr (BIASED) {
-      const double b = open ? (double)a.bias[e0 + v] : 0.0;
-      key[v] = open ? key_of(1.0 / (1.0 + exp(-(double)l[v])) + b) : 0;
-    } else {
-      key[v] = open ? key_of(l[v]) : 0;
-    }
-  }
-  int id = -1;           // lane j: the expert of slot j and its logit
-  float logit = 0.0f;
-  for (int j = 0; j < a.top; ++j) {
+  for (int j = 0; j < n; ++j) {
     Key best = key[0];
     int at = 0;
 #pragma unroll
@@ -100,21 +89,75 @@ __global__ __launch_bounds__(256) void k_moe_route(RouteArgs a) {
       best = key[v] > best ? key[v] : best;
     }
     const Key m = wave_max(best);
-    if (m == 0) break;   // no expert left
+    if (m == 0) return;   // no expert left
     const int win = __ffsll((unsigned long long)__ballot(best == m)) - 1;
-    const int idx = __builtin_amdgcn_readlane(at, win);
-    float lv = l[0];
-#pragma unroll
-    for (int v = 1; v < NV; ++v) lv = idx == v ? l[v] : lv;
-    lv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lv), win));
-    if (lane == j) {
-      id = win * NV + idx;
-      logit = lv;
-    }
+    const int which = __builtin_amdgcn_readlane(at, win);
+    if (!won(j, m, win, which)) return;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      if (lane == win && v == idx) key[v] = 0;
+      if (lane == win && v == which) key[v] = 0;
   }
+}
+
+// NV: experts a lane; BIASED: the choice by biased sigmoid scores
+template <int NV, bool BIASED>
+__global__ __launch_bounds__(256) void k_moe_route(RouteArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= a.t) return;   // whole waves, and no barrier below
+  const float* row = a.logits + t * a.ldl;
+  const int e0 = lane * NV, E = (int)a.experts;
+  float l[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) l[v] = row[e0 + v < E ? e0 + v : E - 1];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) l[v] = e0 + v < E ? l[v] : -__builtin_inff();
+  int id = -1;           // lane j: the expert of slot j
+  auto take = [&](int j, int win, int which) { id = lane == j ? win * NV + which : id; };
+  auto open = [&](int v) { return l[v] > -__builtin_inff(); };   // false for NaN
+  if constexpr (BIASED) {
+    // first in fp32, one round more than slots: the sigmoid's exponent, exponential, sum and
+    // reciprocal leave it within 4 * 2^-24, the sum with the bias within 2^-24 of its size, so where
+    // every score lies over 2^-20 (times the larger size, where that passes 1) above the next one,
+    // the order is that of fp64.  Otherwise (two scores of 256 next to the top, in one of 1000
+    // tokens) it is decided in fp64.  8192 x 256, 8 chosen: 11.3 us, all in fp64 14.7.
+    float bias[NV];
+    uint32_t key[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) bias[v] = a.bias[e0 + v < E ? e0 + v : E - 1];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[v] * -1.442695041f));
+      key[v] = open(v) ? key_of(s + bias[v]) : 0;
+    }
+    bool clear = true;
+    float last = 0.0f;
+    rounds<NV>(key, a.top + 1, [&](int j, uint32_t m, int win, int which) {
+      const float now = value_of(m);
+      if (j > 0) clear = last - now > 0x1p-20f * fmaxf(1.0f, fmaxf(__builtin_fabsf(last), __builtin_fabsf(now)));
+      last = now;
+      if (clear && j < a.top) take(j, win, which);
+      return clear;
+    });
+    if (!clear) {
+      uint64_t exact[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) exact[v] = open(v) ? key_of(1.0 / (1.0 + exp(-(double)l[v])) + (double)bias[v]) : 0;
+      rounds<NV>(exact, a.top, [&](int j, uint64_t, int win, int which) {
+        take(j, win, which);
+        return true;
+      });
+    }
+  } else {
+    uint32_t key[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) key[v] = open(v) ? key_of(l[v]) : 0;
+    rounds<NV>(key, a.top, [&](int j, uint32_t, int win, int which) {
+      take(j, win, which);
+      return true;
+    });
+  }
+  const float logit = id < 0 ? 0.0f : row[id];
   float w, total;
   if (a.sigmoid) {
     w = id < 0 ? 0.0f : 1.0f / (1.0f + expf(-logit));

@@ -341,3 +341,22 @@ def test_streams_and_other_devices():
                 lambda: S.nm_moe_route(x, ids.cpu(), w), lambda: S.nm_moe_route(x.cpu(), ids, w, stream=side)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_route_scores_next_to_each_other():
+    """Biased scores that fp32 cannot tell apart, or takes for equal: the order is that of 64 bits."""
+    rng = np.random.default_rng(16)
+    t, e = 300, 64
+    l = (2 * rng.standard_normal((t, e))).astype(np.float32)
+    # biases that bring many experts' scores of the first token to within a few 2^-25 of one value
+    bias = (1.0 - 1.0 / (1.0 + np.exp(-l[0].astype(np.float64)))).astype(np.float32)
+    for r in range(1, t):
+        # tokens near the first one: their scores spread by fractions of a step, and ties among them
+        l[r] = np.nextafter(l[0], np.float32(rng.choice([-9, 9])), dtype=np.float32) if r % 3 else l[0]
+        pick = rng.random(e) < 0.2
+        l[r, pick] = rng.standard_normal(int(pick.sum())).astype(np.float32)
+    for top in (1, 8, 32):
+        check_route(l, top, S.NM_ROUTER_SIGMOID, bias)
+    check_route(l, 8, S.NM_ROUTER_SIGMOID, np.zeros(e, np.float32))
+    check_route(l, 8, S.NM_ROUTER_SIGMOID, (bias * 1000).astype(np.float32))
+    check_route(np.tile(l[:1], (1, 2)), 20, S.NM_ROUTER_SIGMOID, np.tile(bias, 2))
