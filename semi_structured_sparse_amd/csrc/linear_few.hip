@@ -9,6 +9,10 @@
 // The waves' partial tiles are added in LDS, in their order, and leave through the epilogue.
 // Where row blocks are too few to fill the chip the reduction is also cut across workgroups,
 // whose partial sums a second kernel adds, again in order: a call's bits do not depend on timing.
+// Sums are fp32 throughout; a bf16 output is rounded once, behind the epilogue.
+//
+// 1 x 4096 x 4096 from HBM 9.9 us (floor 5.9 at 5.7 TB/s, the rest launch, two memory latencies and the
+// sum in LDS; 9.4 a call with weights from the cache), 2:4 9.0; 1 x 4096 x 14336 25.0 (floor 20.6).
 //
 // Operands: v_mfma_f32_16x16x32_bf16 takes from lane l eight values of row l % 16 at position
 // 8 (l / 16) of a 32-position step, both sides alike.  v_smfmac_f32_16x16x64_bf16 takes the eight

@@ -101,13 +101,7 @@ __device__ __forceinline__ void each(F&& f) {
   }
 }
 
-// What a wave does with its finished sums: FI x FJ blocks of 16 x 16, lane (fr, fq) = (lane & 15,
-// lane >> 4) holding outputs 4 fq + [0, 4) of each block's range for token fr.  ob_w, tb_w: the wave's
-// first output and token.  With a split reduction the sums go to part.  Otherwise 16 JB tokens at
-// a time are turned through the wave's own LDS at `mine` (rows of W outputs, 16-byte piece c of row
-// r at c ^ (r & (W / 4 - 1))): neighbouring lanes hold neighbouring outputs of a row, four each
-// where rows of y and the residual keep that alignment, one each otherwise.  The residual's
-// loads go out together, ahead of the turn.
+// The parts that a wave's FI x FJ blocks of 16 x 16 sums leave in: BI x JB blocks each.
 template <int FI, int FJ>
 struct Turn {
   static constexpr int BI = FI < 4 ? FI : 4, W = 16 * BI;   // blocks and outputs of a row
@@ -123,7 +117,8 @@ struct Turn {
 // each where rows of y and of the residual keep that alignment, one each otherwise.  One wave may
 // have its SIMD for itself, so what costs instructions is done once (types, addresses), and the
 // next part's residual is loaded ahead of the use of this one's.  The parts run in a loop, each with
-// its own put: unrolled, a 256 x 256 tile's epilogue took 26 us instead of 9.
+// its own put (unrolled, their code is eight times as long: 8192 x 14336 x 4096, gelu and bias, 736
+// against 723 us).  bf16 outputs are rounded once, from the fp32 sum with bias, activation and residual.
 template <int W, int ROWS>
 struct Emit {
   static constexpr int PC = W / 4, RP = 64 / PC, NP = ROWS / RP;   // pieces of a row; rows of a pass; passes
@@ -347,6 +342,14 @@ __device__ __forceinline__ void lin_finish(const f32x4 (&acc)[FI][FJ], const Lin
 }
 
 // BM x BN: weight rows by tokens of a tile; WM x WN waves; NST stages of KM chunks.
+//
+// Between the streaming kernel and the 256 x 256 tiles: too few tiles to fill the chip, so a step costs
+// what its loads' latency leaves behind the ring, whatever it holds, and tiles and reduction ranges
+// are chosen by estimated time (mid_plan).  Two chunks a step where the stages fit two workgroups a CU
+// or the tile is short of work (40 x 4096 x 14336 2:4: 44 us with one chunk a step and the
+// largest tile that gives 192 workgroups, 26 so).  Measured from HBM: 40 x 4096 x 14336 2:4 26.3 us (19 with its weights in the cache: 15.2 and the
+// ranges' sum 4.0), floor 11.9 at 5.7 TB/s; 777 x 1025 x 1999 14.7, of it a step's load, launch and
+// epilogue about 5, the rest 32 steps of 0.3.
 template <int BM, int BN, int WM, int WN, bool SP, int NST, int KM>
 __global__ __launch_bounds__(64 * WM * WN) void k_lin_tile(
     const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ w, int64_t ldw,
@@ -584,6 +587,12 @@ __device__ __forceinline__ float acc_read(float a) {
 // the matrix instructions, which a phase has 16 of.
 // v_mfma_f32_32x32x16_bf16: lane (c, h) = (lane & 31, lane >> 5) holds values 8 h + [0, 8) of a
 // 16-position part of row c, of either side; its sums are rows 8 (v / 4) + 4 h + v % 4 of token c.
+//
+// Bound by power: the matrix pipe is busy in 82% of cycles without an epilogue, 73% with bias and
+// gelu, and the card runs them at 1.45 GHz; the same loop with nothing but its matrix instructions
+// takes 506-528 us at 8192 x 4096 x 14336, with nothing but its loads 518-534.  Measured (cards differ
+// by 5%): 8192 x 4096 x 14336 684 us (8 waves of 64 x 128 on two stages 722), 8192 x 14336 x 4096 with
+// bias and gelu 741-780 (without 707-735), 4096 x 4096 x 4096 104 (110).
 __global__ __launch_bounds__(256) void k_lin_big(
     const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ w, int64_t ldw, int64_t T, int64_t O, int k,
     LinEpi epi, int tiles_m, int tiles_n, int group) {
@@ -767,6 +776,10 @@ __global__ __launch_bounds__(256) void k_lin_big(
 //  * A step of 64 positions is two phases.  When a step begins, its operands are in registers and the
 //    next step's have landed: one wait, one barrier, and the stage takes the requests of the step
 //    after the next two.
+// The matrix pipe is busy in 44% of cycles, LDS in 24% (11% of these conflicts, in the positions), at
+// 1.78 GHz (bias and gelu, 8192 x 14336 x 4096): less than the dense product's share, since a
+// step's barrier comes after half its matrix cycles.  Measured: 8192 x 14336 x 4096 528 us (8
+// waves of 64 x 128 on two stages 656), 8192 x 4096 x 14336 504 (713), 4096 x 4096 x 4096 78 (94).
 __global__ __launch_bounds__(256) void k_lin_big24(
     const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ w, int64_t ldw,
     const uint8_t* __restrict__ meta, int64_t T, int64_t O, int k, LinEpi epi, int tiles_m, int tiles_n, int group) {

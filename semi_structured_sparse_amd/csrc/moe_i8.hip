@@ -14,6 +14,15 @@
 // and a token's place in its item is its rank in the mask.  Each workgroup of the first kernel
 // works that out for itself (a kernel of its own for it would cost a launch); one of them writes
 // it down for the kernels behind it.
+//
+// Three kernels: the hidden rows' codes need a row's largest value, which only all of the gate and up
+// products of an expert give, and the down products read codes.  The row's codes and scale are
+// rounded as nm_quant_i8 rounds them, from bf16 hidden values; everything behind is fp32.
+//
+// Bound by the weights' bytes.  Measured (us, weights from HBM; gate and up + codes + down): 1 token 2/8
+// 4096 x 14336 71, 43 + 4.8 + 23 (5.0 TB/s; floor 62 at 5.7); 64 tokens 6/64 4096 x 1408 215, 136 + 4.7 +
+// 74 (5.2 TB/s; floor 194); 8 tokens 8/64 2:4 2048 x 1024 48, 25 + 3.9 + 15 and 2.1 for the parts' sum
+// (floor 29: each kernel is only a few memory latencies long).
 #include "i8_device.h"
 #include "layer_launch.h"
 
@@ -267,7 +276,9 @@ __device__ __forceinline__ void moe_store(const MoeArgs& a, float v, int64_t tok
 // Down products of every item for 16 outputs, each token's summed with its weights.  The items'
 // steps are one sequence of batches that the waves (of all blockIdx.y, where there are too few
 // blocks of outputs to fill the chip) share in contiguous parts; a wave adds what it has of an
-// item to its own sums in LDS, and the waves' sums are added in their order.
+// item to its own sums in LDS, and the waves' sums are added in their order.  Batches of two steps
+// (64 tokens 6/64 4096 x 1408 215 us a layer, with six 220), four for 2:4 items of 16, whose steps are
+// half as many.
 template <int TB, bool SP>
 __global__ __launch_bounds__(512) void k_moe_down(MoeArgs a, Plan p, int t) {
   constexpr int STEP = SP ? 128 : 64;
@@ -402,7 +413,9 @@ __global__ __launch_bounds__(256) void k_moe_sum(MoeArgs a, const float* __restr
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
-// Parts that the down products' item sequence is cut in.
+// Parts that the down products' item sequence is cut in: up to a workgroup a CU, eight steps a wave at
+// least (8 tokens 8/64 2:4 2048 x 1024, 128 blocks of outputs: 1 / 2 / 4 parts 57.5 / 49.3 / 51.5 us a
+// layer).
 int down_parts(int64_t t, int64_t experts, int64_t top, int64_t hidden, int64_t inter) {
   const int64_t blocks = (hidden + 15) / 16, slots = t * top, asked = slots < experts ? slots : experts;
   int64_t parts = blocks > 0 ? 256 / blocks : 1;
