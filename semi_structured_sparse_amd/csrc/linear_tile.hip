@@ -42,6 +42,13 @@ struct Stage {
   unsigned char *a, *b;
 };
 
+// The place of this workgroup in the order of all: workgroups go to the 8 XCDs in turn, and each XCD
+// runs a contiguous range.
+__device__ __forceinline__ int by_xcd() {
+  const int n = (int)gridDim.x, x = blockIdx.x & 7;
+  return x * (n >> 3) + min(x, n & 7) + (int)(blockIdx.x >> 3);
+}
+
 __device__ __forceinline__ void bar() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -376,9 +383,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_lin_tile(
   const int fr = lane & 15, fq = lane >> 4;
 
   const int ntiles = tiles_m * tiles_n;
-  const int kpart = __builtin_amdgcn_readfirstlane(blockIdx.x / ntiles);
-  int lin = blockIdx.x - kpart * ntiles;
-  if ((ntiles & 7) == 0 && gridDim.x == (unsigned)ntiles) lin = (blockIdx.x & 7) * (ntiles >> 3) + (blockIdx.x >> 3);
+  const int place = by_xcd();
+  const int kpart = __builtin_amdgcn_readfirstlane(place / ntiles);
+  const int lin = place - kpart * ntiles;
   const int band = lin / (group * tiles_n);
   const int band_w = min(group, tiles_m - band * group);
   const int inband = lin - band * group * tiles_n;
@@ -604,9 +611,7 @@ __global__ __launch_bounds__(256) void k_lin_big(
   const int wmi = wave & 1, wni = wave >> 1;
   const int c = lane & 31, h = lane >> 5;
 
-  const int ntiles = tiles_m * tiles_n;
-  int lin = blockIdx.x;
-  if ((ntiles & 7) == 0) lin = (blockIdx.x & 7) * (ntiles >> 3) + (blockIdx.x >> 3);
+  const int lin = by_xcd();
   const int band = lin / (group * tiles_n);
   const int band_w = min(group, tiles_m - band * group);
   const int inband = lin - band * group * tiles_n;
@@ -792,9 +797,7 @@ __global__ __launch_bounds__(256) void k_lin_big24(
   const int wmi = wave & 1, wni = wave >> 1;
   const int c = lane & 31, h = lane >> 5;
 
-  const int ntiles = tiles_m * tiles_n;
-  int lin = blockIdx.x;
-  if ((ntiles & 7) == 0) lin = (blockIdx.x & 7) * (ntiles >> 3) + (blockIdx.x >> 3);
+  const int lin = by_xcd();
   const int band = lin / (group * tiles_n);
   const int band_w = min(group, tiles_m - band * group);
   const int inband = lin - band * group * tiles_n;
