@@ -18,8 +18,8 @@
 // One pass: a row's p stay in registers between the reductions (the largest |p| and the sum
 // cross the workgroup together) and the outputs.  y is rounded to bf16 once; the codes come from the
 // unrounded p.  Bound by memory: 4095 x 4096 bf16 with residual, sum, y and the 6:8 lift 34.5 us (5.6
-// TB/s; a copy of 512 MB 5.35), 8192 x 8192 8:16 103 (4.5 TB/s: 16 values' sorting network a lane
-// behind the loads); one row of 4096 3.7, a launch and two memory latencies.
+// TB/s; a copy of 512 MB 5.35), 8192 x 8192 86 (5.5 TB/s), 8:16 94 (5.0); one row of 4096 3.7, a launch
+// and two memory latencies.
 #include "i8_device.h"
 #include "layer_launch.h"
 
@@ -58,32 +58,132 @@ __device__ __forceinline__ uint32_t codes4(const float* p, const RowCode& c) {
   return __builtin_amdgcn_perm(c1, c0, 0x0C0C0400u) | __builtin_amdgcn_perm(c3, c2, 0x04000C0Cu);
 }
 
-// Keep bits of the n largest magnitudes of a group, ties to the lower index: the n-th largest
-// key, every key above it, and of the equal ones the first.
-template <int M, int NT>
-__device__ __forceinline__ uint32_t keep_bits(const float* p, int n) {
-  uint32_t k[M], s[M];
+// The value of the lane that PERM (two bits a lane) names in each quad.
+template <int PERM>
+__device__ __forceinline__ uint32_t quad(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, PERM, 0xF, 0xF, true);
+}
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kTurn = 0x1B;   // lanes 1 0 3 2, 2 3 0 1, 3 2 1 0
+
+// Eight keys that fall, then rise or the other way round, into falling order.
+__device__ __forceinline__ void settle8(uint32_t (&s)[8]) {
 #pragma unroll
-  for (int i = 0; i < M; ++i) s[i] = k[i] = __float_as_uint(p[i]) & 0x7FFFFFFFu;
-  sort_desc_oem<M>(s);
-  uint32_t tau = s[NT > 0 ? NT - 1 : 0];
-  if constexpr (NT > 0) {
-    n = NT;
+  for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) {
+        const uint32_t x = s[i], y = s[i + d];
+        s[i] = max(x, y);
+        s[i + d] = min(x, y);
+      }
+}
+// s against PERM's lane, its keys turned round: the larger ones where `up`, else the smaller ones.
+// Of two falling runs these are their larger and their smaller half.
+template <int PERM, bool TURN>
+__device__ __forceinline__ void halve(uint32_t (&s)[8], bool up) {
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = quad<PERM>(s[TURN ? 7 - i : i]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = up ? max(s[i], o[i]) : min(s[i], o[i]);
+}
+
+// What a group keeps, its n largest magnitudes, ties to the lower index: every value whose key (the
+// bits of |p|) is at least tau, the n-th largest, but not those of drop, the last of equal ones where
+// the (n + 1)-th is tau too.  A lane holds 8 values: two groups of 4 (G = 0, 1), a group of 8, half
+// of one of 16, a quarter of one of 32.  Wide groups are sorted within the lane and then across
+// lanes by halving: where n = M / 2 (NK), the larger half's least key is tau.  (A whole group a lane
+// takes the row in pieces with gaps between the lanes', for loads and stores alike: 8192 x 8192 8:16
+// 107 us instead of 94, 16:32 145 instead of
+// 98.)
+struct Kept {
+  uint32_t tau, drop;
+};
+template <int M, int NK>
+__device__ __forceinline__ Kept kept(const float* p, int n) {
+  constexpr int W = M < 8 ? M : 8;   // of the group in this lane
+  const int lane = threadIdx.x & 63;
+  if constexpr (NK > 0) n = NK;
+  uint32_t k[W], s[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) s[i] = k[i] = __float_as_uint(p[i]) & 0x7FFFFFFFu;
+  sort_desc_oem<W>(s);
+  uint32_t tau, next;
+  if constexpr (M > 8 && NK == M / 2) {
+    if constexpr (M == 32) {
+      halve<kSwap1, true>(s, (lane & 1) == 0);
+      settle8(s);
+    }
+    constexpr int FAR = M == 32 ? kTurn : kSwap1;
+    uint32_t lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo[i] = quad<FAR>(s[7 - i]);
+    tau = max(s[0], lo[0]);
+    next = min(s[0], lo[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      tau = min(tau, max(s[i], lo[i]));
+      next = max(next, min(s[i], lo[i]));
+    }
+    if constexpr (M == 32) {
+      tau = min(tau, quad<kSwap1>(tau));
+      next = max(next, quad<kSwap1>(next));
+    }
   } else {
+    if constexpr (M > 8) {
+      halve<kSwap1, true>(s, (lane & 1) == 0);
+      settle8(s);
+    }
+    if constexpr (M == 32) {
+      halve<kTurn, true>(s, (lane & 2) == 0);
+      halve<kSwap1, false>(s, (lane & 1) == 0);
+      settle8(s);
+    }
+    // rank n - 1 and n of the group: its lane q holds ranks [8 q, 8 q + 8)
+    const int q = M == 32 ? lane & 3 : M == 16 ? lane & 1 : 0;
+    tau = next = 0u;
 #pragma unroll
-    for (int j = 1; j < M; ++j) tau = j == n - 1 ? s[j] : tau;
+    for (int j = 0; j < W; ++j) {
+      tau = 8 * q + j == n - 1 ? s[j] : tau;
+      next = 8 * q + j == n ? s[j] : next;
+    }
+    if constexpr (M > 8) {
+      tau |= quad<kSwap1>(tau);
+      next |= quad<kSwap1>(next);
+    }
+    if constexpr (M == 32) {
+      tau |= quad<kSwap2>(tau);
+      next |= quad<kSwap2>(next);
+    }
   }
-  int left = n;
+  Kept o{tau, 0u};
+  if (__any(next == tau && tau != 0u)) {   // zeros are zeros, kept or dropped
+    int above = 0, equal = 0;
 #pragma unroll
-  for (int i = 0; i < M; ++i) left -= k[i] > tau ? 1 : 0;
-  uint32_t bits = 0;
+    for (int i = 0; i < W; ++i) {
+      above += k[i] > tau ? 1 : 0;
+      equal += k[i] == tau ? 1 : 0;
+    }
+    int before = 0;   // equal ones in the group's earlier lanes
+    if constexpr (M > 8) {
+      above += (int)quad<kSwap1>((uint32_t)above);
+      const int other = (int)quad<kSwap1>((uint32_t)equal);
+      before = lane & 1 ? other : 0;
+      if constexpr (M == 32) {
+        above += (int)quad<kSwap2>((uint32_t)above);
+        const int far = (int)quad<kSwap2>((uint32_t)(equal + other));
+        before += lane & 2 ? far : 0;
+      }
+    }
+    int left = n - above - before;
 #pragma unroll
-  for (int i = 0; i < M; ++i) {
-    const bool eq = k[i] == tau;
-    bits |= (k[i] > tau || (eq && left > 0) ? 1u : 0u) << i;
-    left -= eq ? 1 : 0;
+    for (int i = 0; i < W; ++i) {
+      const bool eq = k[i] == tau;
+      o.drop |= (eq && left <= 0 ? 1u : 0u) << i;
+      left -= eq ? 1 : 0;
+    }
   }
-  return bits;
+  return o;
 }
 
 __device__ __forceinline__ void widen(const uint4& d, float* v) {
@@ -116,12 +216,11 @@ __device__ __forceinline__ uint4 narrow(const float* v) {
   return make_uint4(e[0], e[1], e[2], e[3]);
 }
 
-// UN units of PU pieces of 8 values a thread, the workgroup as many waves as the row needs.
+// P pieces of 8 values a thread, the workgroup as many waves as the row needs.
 // WAVE: a row per wave, four rows a workgroup.  SEL: 0 none, M the group width (NK > 0: n known
 // at compile time).  LIFT: 0 none, 4 the N = 4 lift from registers, 1 any N through LDS.
-template <bool WAVE, int UN, int SEL, int NK, int LIFT>
+template <bool WAVE, int P, int SEL, int NK, int LIFT>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_rmsnorm_i8(NormArgs a) {
-  constexpr int PU = SEL > 8 ? SEL / 8 : 1, P = UN * PU;
   __shared__ uint32_t red_max[WAVE ? 1 : 16];
   __shared__ double red_sum[WAVE ? 1 : 16];
   extern __shared__ __align__(16) unsigned char codes[];   // LIFT == 1: the rows' codes
@@ -130,7 +229,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_rmsnorm_i8(NormArgs a) {
   const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (WAVE && row >= a.rows) return;   // whole waves; no barrier below for these
   const int k = (int)a.k;
-  auto at = [&](int i) { return ((i / PU * NT + tid) * PU + i % PU) * 8; };   // first value of piece i
+  auto at = [&](int i) { return (i * NT + tid) * 8; };   // first value of piece i
 
   // every load of the row first: rows are readable in whole pieces (leading dimensions % 8 == 0)
   uint4 xa[P], xb[P], ra[P], rb[P];
@@ -236,13 +335,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_rmsnorm_i8(NormArgs a) {
     }
   }
   // the normed row's factor needs the reductions, the selection does not: it runs while the other
-  // waves' arrive.  Dropped values are zeroed after the normed row is written: their bits wait.
-  uint32_t keep[SEL > 0 ? UN : 1][SEL == 4 ? 2 : 1];
+  // waves' arrive.  Dropped values are zeroed after the normed row is written.
+  constexpr int GROUPS = SEL == 4 ? 2 : 1, GW = SEL == 4 ? 4 : 8;   // of a piece, and their values
+  Kept keep[SEL > 0 ? P : 1][GROUPS];
   if constexpr (SEL > 0) {
 #pragma unroll
-    for (int u = 0; u < UN; ++u)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-      for (int g = 0; g < (SEL == 4 ? 2 : 1); ++g) keep[u][g] = keep_bits<SEL, NK>(&p[u * PU][0] + g * SEL, a.n);
+      for (int g = 0; g < GROUPS; ++g) keep[i][g] = kept<SEL, NK>(p[i] + g * GW, a.n);
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) {
@@ -289,10 +389,21 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_rmsnorm_i8(NormArgs a) {
   }
   if constexpr (SEL > 0) {
 #pragma unroll
-    for (int u = 0; u < UN; ++u)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-      for (int e = 0; e < 8 * PU; ++e)
-        if (!((keep[u][SEL == 4 ? e / 4 : 0] >> (SEL == 4 ? e % 4 : e)) & 1u)) p[u * PU + e / 8][e % 8] = 0.0f;
+      for (int g = 0; g < GROUPS; ++g) {
+        const Kept w = keep[i][g];
+#pragma unroll
+        for (int e = 0; e < GW; ++e) {
+          float& v = p[i][g * GW + e];
+          v = (__float_as_uint(v) & 0x7FFFFFFFu) >= w.tau ? v : 0.0f;
+        }
+        if (__any(w.drop != 0u)) {
+#pragma unroll
+          for (int e = 0; e < GW; ++e)
+            if ((w.drop >> e) & 1u) p[i][g * GW + e] = 0.0f;
+        }
+      }
   }
 
   int8_t* qr = a.q + row * a.ldq;
@@ -344,7 +455,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_rmsnorm_i8(NormArgs a) {
   }
 }
 
-template <bool WAVE, int UN, int SEL, int NK, int LIFT>
+template <bool WAVE, int P, int SEL, int NK, int LIFT>
 hipError_t launch_n(int threads, const NormArgs& a, hipStream_t s) {
   const size_t lds = LIFT == 1 ? (size_t)((a.k + 15) / 16 * 16) * (WAVE ? 4 : 1) : 0;
   constexpr int64_t kRows = (1 << 22) - 4;   // of a launch: a grid holds under 2^32 threads
@@ -357,7 +468,7 @@ hipError_t launch_n(int threads, const NormArgs& a, hipStream_t s) {
     if (a.y != nullptr) b.y = a.y + r * a.ldy;
     b.q = a.q + r * a.ldq;
     b.scale = a.scale + r;
-    k_rmsnorm_i8<WAVE, UN, SEL, NK, LIFT>
+    k_rmsnorm_i8<WAVE, P, SEL, NK, LIFT>
         <<<dim3((unsigned)(WAVE ? (b.rows + 3) / 4 : b.rows)), dim3(WAVE ? 256 : threads), lds, s>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -365,18 +476,16 @@ hipError_t launch_n(int threads, const NormArgs& a, hipStream_t s) {
   return hipSuccess;
 }
 
-// A row per wave up to 2048 values (4 pieces a lane), no barrier; longer rows 2 pieces a thread up to 4096
-// values (4 for groups of 32, whose unit is 4), 4 beyond.
+// A row per wave up to 2048 values (4 pieces a lane), no barrier; longer rows 2 pieces a thread up to
+// 12288 values, 4 beyond (us, 2 / 4 pieces: 8192 x 5120 58 / 62, 8192 x 8192 86 / 90, 8:16 94 / 93, 6000 x
+// 10240 86 / 106, 4096 x 12288 69 / 85, 8:16 74 / 96, 6:8 lift 73 / 88, 4096 x 14336 6:8 lift 96 / 94, 4096 x
+// 16384 8:16 127 / 99: 1024 threads of over 64 registers are alone on a CU).
 template <int SEL, int NK, int LIFT>
 hipError_t by_length(const NormArgs& a, hipStream_t s) {
-  constexpr int PU = SEL > 8 ? SEL / 8 : 1;
-  if (a.k <= 2048) return launch_n<true, 4 / PU, SEL, NK, LIFT>(256, a, s);
-  const int pieces = PU <= 2 && a.k <= 4096 ? 2 : 4;
+  if (a.k <= 2048) return launch_n<true, 4, SEL, NK, LIFT>(256, a, s);
+  const int pieces = a.k <= 12288 ? 2 : 4;
   const int threads = (int)(((a.k + 15) / 16 * 16 + 512 * pieces - 1) / (512 * pieces) * 64);
-  if constexpr (PU <= 2) {
-    if (pieces == 2) return launch_n<false, 2 / PU, SEL, NK, LIFT>(threads, a, s);
-  }
-  return launch_n<false, 4 / PU, SEL, NK, LIFT>(threads, a, s);
+  return pieces == 2 ? launch_n<false, 2, SEL, NK, LIFT>(threads, a, s) : launch_n<false, 4, SEL, NK, LIFT>(threads, a, s);
 }
 
 }  // namespace

@@ -123,6 +123,20 @@ def test_norm_selected(m):
             check_norm(x, "f32", r, "f32", w, n=n, m=m)
 
 
+@pytest.mark.parametrize("m", [4, 8, 16, 32])
+def test_norm_selected_ties(m):
+    """Groups of a few values only, so that the border of what is kept falls between equal ones, which
+    several lanes may hold; every n, rows of a wave's and of a workgroup's length."""
+    rng = np.random.default_rng(50 + m)
+    for k in (32 * 13, 32 * 90, 32 * 200):
+        print("norm ties", m, k, flush=True)
+        for n in range(1, m + 1):
+            x = rng.integers(-3, 4, (4, k)).astype(np.float32)    # exact in either type; zeros too
+            x[1] = np.abs(x[1]) + 1
+            x[2] *= rng.random(k) < 0.2
+            check_norm(x, "bf16", n=n, m=m, y=False)
+
+
 @pytest.mark.parametrize("ns", [3, 4, 5, 6, 7, 8])
 def test_norm_lifted(ns):
     rng = np.random.default_rng(ns)
