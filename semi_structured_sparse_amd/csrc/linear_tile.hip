@@ -1007,12 +1007,13 @@ struct MidPlan {
 };
 
 // The tile and the number of reduction ranges of least estimated time:
-//   chunks of a range * time of one * rounds of 256 workgroups (one per CU; the weights' stream at 5
-//   TB/s where that is longer), and where the reduction is split 2.8 us for the second kernel and
-//   its partial sums, written and read, at 3.2 TB/s.
+//   chunks of a range * time of one * rounds of 256 workgroups (whole ones where the stages leave a
+//   CU one workgroup; the weights' stream at 5 TB/s where that is longer), and where the reduction
+//   is split 2.8 us for the second kernel and its partial sums, written and read, at 3.2 TB/s.
 // A chunk's time is that of its loads' latency behind the barrier, whatever it holds, up to 256
 // workgroups: measured (with weights from HBM) and fitted with the other constants over 28 sizes of
-// 16 to 777 tokens, 16 plans each: the plan chosen is 2% slower than the best of the 16 on average.
+// 16 to 777 tokens.  Over 48 others of 40 to 3000 tokens the plan chosen is 1.4% slower than the best
+// of 16 on average (with parts of a round throughout 4.5%: 600 x 4096 x 4096 128 x 64 54, 128 x 128 40 us).
 // Some of them (us, tile x ranges): 40 x 4096 x 14336 64 x 32 x 2 40.6, 64 x 64 x 4 30.7, 128 x 64 x 8
 // 31.1, unsplit 59-120; 128 x 4096 x 14336 64 x 32 58.5, 64 x 64 x 2 44.6, 128 x 64 x 4 42.6, 128 x 128 x
 // 8 40.3; 64 x 14336 x 4096 64 x 64 31.9, x 2 36.6, 64 x 32 38.0; 600 x 2048 x 2048 128 x 64 13.9, 64 x
@@ -1023,6 +1024,7 @@ MidPlan mid_plan(int64_t t, int64_t o, int64_t k, bool sparse) {
   constexpr int kBM[4] = {128, 128, 64, 64}, kBN[4] = {128, 64, 64, 32};
   constexpr int kRanges[8] = {1, 2, 3, 4, 6, 8, 12, 16};
   constexpr double kChunk[2][4] = {{0.60, 0.45, 0.31, 0.255}, {0.50, 0.34, 0.286, 0.168}};   // us
+  constexpr bool kAlone[2][4] = {{true, true, false, true}, {true, true, true, false}};   // on a CU
   const int64_t chunks = (k + 63) / 64;
   const double stream = (double)o * (double)k * (sparse ? 1.125 : 2.0) / 5.0e6;
   MidPlan best{3, 1};
@@ -1031,7 +1033,7 @@ MidPlan mid_plan(int64_t t, int64_t o, int64_t k, bool sparse) {
     const double tiles = (double)((o + kBM[sh] - 1) / kBM[sh]) * (double)((t + kBN[sh] - 1) / kBN[sh]);
     for (int r : kRanges) {
       if (r > 1 && (chunks < 8 * r || tiles * r > 1024)) break;
-      const double rounds = tiles * r <= 256 ? 1.0 : tiles * r / 256;
+      const double full = tiles * r / 256, rounds = full <= 1.0 ? 1.0 : kAlone[sparse][sh] ? __builtin_ceil(full) : full;
       double us = (double)((chunks + r - 1) / r) * kChunk[sparse][sh] * rounds;
       if (us < stream) us = stream;
       if (r > 1) us += 2.8 + (double)r * (double)t * (double)o * 8 / 3.2e6;
