@@ -355,7 +355,7 @@ __device__ __forceinline__ void lin_finish(const f32x4 (&acc)[FI][FJ], const Lin
 // are chosen by estimated time (mid_plan).  Two chunks a step where the stages fit two workgroups a CU
 // or the tile is short of work (40 x 4096 x 14336 2:4: 44 us with one chunk a step and the
 // largest tile that gives 192 workgroups, 26 so).  Measured from HBM: 40 x 4096 x 14336 2:4 26.3 us (19 with its weights in the cache: 15.2 and the
-// ranges' sum 4.0), floor 11.9 at 5.7 TB/s; 777 x 1025 x 1999 14.7, of it a step's load, launch and
+// ranges' sum 4.0), floor 11.9 at 5.7 TB/s; 777 x 1025 x 1999 14.3, of it a step's load, launch and
 // epilogue about 5, the rest 32 steps of 0.3.
 template <int BM, int BN, int WM, int WN, bool SP, int NST, int KM>
 __global__ __launch_bounds__(64 * WM * WN) void k_lin_tile(
