@@ -729,11 +729,13 @@ typedef enum { NM_ROUTER_SOFTMAX = 0, NM_ROUTER_SIGMOID = 1 } nm_router;
  * product, nm_linear or nm_spmm).  Of the experts whose logit is neither -inf nor NaN the `top`
  * with the largest score are chosen, the largest first, ties to the lower index.
  *   NM_ROUTER_SOFTMAX  score = logit;  weight = e^logit / sum over all experts e^logit
- *   NM_ROUTER_SIGMOID  score = weight = 1 / (1 + e^-logit); with a bias score = that + bias[e] in
- *                      fp64, for the choice alone
- * then, with renormalize = 1, weights are divided by the sum of the chosen ones, and multiplied
- * by `scale`.  A slot that no expert is left for gets the id -1 and the weight 0 (all slots of a
- * row whose logits are all -inf); weights whose sum is 0 are 0.
+ *   NM_ROUTER_SIGMOID  score = weight = 1 / (1 + e^-logit), the weight 0 where e^-logit passes fp64
+ *                      (logits below -709.78); with a bias score = that + bias[e] in fp64, for
+ *                      the choice alone
+ * then, with renormalize = 1, weights are divided by the sum of the chosen ones (shares hold where
+ * the weights alone would pass the least value of fp32), and multiplied by `scale`.  A slot that no
+ * expert is left for gets the id -1 and the weight 0 (all slots of a row whose logits are all -inf);
+ * weights whose sum is 0 are 0.
  *   logits   fp32 [t][ldl], ldl >= experts;  bias fp32 [experts], finite, or NULL; with softmax:
  *            NM_EUNSUPPORTED
  *   ids      int32 [t][top];  weights fp32 [t][top]

@@ -3,8 +3,8 @@
 //   choice: the `top` experts of largest score, ties to the lower index; the score is the logit,
 //   or with a bias (sigmoid only) 1 / (1 + e^-logit) + bias in fp64, so that experts whose scores
 //   lie next to each other are told apart as the definition tells them
-//   weight: e^(logit - max) / sum over all experts (softmax) or 1 / (1 + e^-logit) (sigmoid), over
-//   the sum of the chosen ones if renormalized, times scale
+//   weight: e^(logit - max) / sum over all experts (softmax) or 1 / (1 + e^-logit) (sigmoid, 0 where
+//   e^-logit passes fp64), over the sum of the chosen ones if renormalized, times scale
 //
 // A wave per token.  Lane l holds the scores of experts [NV l, NV l + NV) as unsigned keys that
 // order like them, 0 for an expert that cannot be chosen (a logit of -inf or NaN).  A round finds
@@ -161,6 +161,15 @@ __global__ __launch_bounds__(256) void k_moe_route(RouteArgs a) {
   float w, total;
   if (a.sigmoid) {
     w = id < 0 ? 0.0f : 1.0f / (1.0f + expf(-logit));
+    if (a.renormalize && __any(id >= 0 && logit < -80.0f)) {
+      // Below -88 the weight passes the least value of fp32, its share of the chosen ones does not: with
+      // 1 / (1 + e^-l) = e^min(l, 0) / (1 + e^-|l|) all of them go over e^min(M, 0), M their largest
+      // logit, so that M's is at least a half.  (-709.7827: the last l whose e^-l fp64 holds.)  A branch:
+      // in every row 8192 x 64 takes 6.4 us instead of 6.0.
+      const float base = fminf(value_of(wave_max(id < 0 ? 0u : key_of(logit))), 0.0f);
+      const bool held = id >= 0 && logit > -709.7827f;
+      w = held ? expf(fminf(logit, 0.0f) - base) / (1.0f + expf(-__builtin_fabsf(logit))) : 0.0f;
+    }
     total = a.renormalize ? wave_sum(w) : 1.0f;
   } else {
     // slot 0 holds the largest logit; a difference of infinities is the largest itself

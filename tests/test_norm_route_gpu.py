@@ -374,3 +374,31 @@ def test_route_scores_next_to_each_other():
     check_route(l, 8, S.NM_ROUTER_SIGMOID, np.zeros(e, np.float32))
     check_route(l, 8, S.NM_ROUTER_SIGMOID, (bias * 1000).astype(np.float32))
     check_route(np.tile(l[:1], (1, 2)), 20, S.NM_ROUTER_SIGMOID, np.tile(bias, 2))
+
+
+def test_route_sigmoid_weights_far_below_zero():
+    """Chosen logits whose sigmoid passes the least fp32 value (below -88.7) keep their shares: those of
+    64 bits, where it is 0 from -709.78 down."""
+    rng = np.random.default_rng(17)
+    l = np.full((64, 40), -np.inf, np.float32)
+    l[0, :3] = -88.0, -89.0, -90.0
+    l[1, 5] = -120.0
+    l[2, 10:20] = -500.0
+    l[3, :8] = -705.0, -705.5, -709.0, -709.75, -709.8, -712.0, -745.0, -1e30
+    l[4, :8] = -710.0 - np.arange(8)                              # every weight is 0
+    l[5, :6] = -0.5, 3.0, -89.0, -104.0, -300.0, -720.0           # one that counts, others that do not
+    l[6, :6] = -1.0, -2.0, -80.0, -87.0, -88.5, -89.0
+    for r in range(7, 64):
+        far = np.float32(-80.0 - 620.0 * rng.random())            # neighbours within some units of a far place
+        l[r] = far - (10.0 * rng.random(40)).astype(np.float32)
+    for top in (1, 3, 8, 32):
+        for bias in (None, np.zeros(40, np.float32), rng.standard_normal(40).astype(np.float32)):
+            print("route far", top, bias is None, flush=True)
+            check_route(l, top, S.NM_ROUTER_SIGMOID, bias)
+            check_route(l, top, S.NM_ROUTER_SIGMOID, bias, scale=2.5)
+            check_route(l, top, S.NM_ROUTER_SIGMOID, bias, renormalize=False)
+    ids, w = torch.empty(1, 3, dtype=torch.int32, device="cuda"), torch.empty(1, 3, device="cuda")
+    S.nm_moe_route(torch.from_numpy(l[:1, :4]).cuda().contiguous(), ids, w, S.NM_ROUTER_SIGMOID)
+    e = np.exp(-np.arange(3.0))
+    e = e / e.sum()
+    assert (np.abs(w[0].double().cpu().numpy() - e) <= (2 * 104 + 40) * U * e).all()   # as in check_route
