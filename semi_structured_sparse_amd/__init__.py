@@ -768,8 +768,9 @@ def nm_glu_i8(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, act=NM_GLU_SILU
 
 def _rows_of(t, dev, rows, cols, whole, ld, kind, name):
     """(pointer, leading dimension, NM_Y_*) of `rows` rows of `cols` fp32 or bf16 values, read or
-    written in pieces of `whole`; ld: None, or a leading dimension in place of the tensor's; kind: the
-    type of raw pointers (None: fp32), which a tensor has to agree with."""
+    written in pieces of `whole` (a last piece past the columns may hold anything, so none of it counts
+    as one); ld: None, or a leading dimension in place of the tensor's; kind: the type of raw pointers
+    (None: fp32), which a tensor has to agree with."""
     if t is None or type(t) is int:
         return t, ld or 0, NM_Y_F32 if kind is None else kind
     st, d = t.stride(), t.dtype
@@ -779,7 +780,9 @@ def _rows_of(t, dev, rows, cols, whole, ld, kind, name):
     r, c = t.shape
     if ld is None:
         ld = st[0] if cols else 0       # of no columns: torch has 1
-    if r < rows or c < cols or c & (whole - 1) or ld != st[0]:
+    if c < cols:
+        raise ValueError(f"{name}: rows of {cols} values are needed")
+    if r < rows or c & (whole - 1) or ld != st[0]:
         _holds(t, rows, cols, whole, ld)
     return t.data_ptr(), ld, have
 
@@ -795,7 +798,8 @@ def _list_of(t, n, dev, kind, name):
 
 
 def _bf16_rows(t, dev, rows, cols, ld, name):
-    """(pointer, leading dimension) of `rows` rows of `cols` bf16 values that are read in pieces of 8."""
+    """(pointer, leading dimension) of `rows` rows of `cols` bf16 values that are read in pieces of 8 (a
+    last piece past the columns may hold anything, so none of it counts as one)."""
     if t is None or type(t) is int:
         return t, ld or 0
     st, sh = t.stride(), t.shape
@@ -803,6 +807,8 @@ def _bf16_rows(t, dev, rows, cols, ld, name):
         _refuse(t, dev, f"{name}: a matrix with contiguous rows of bf16 values is needed")
     if ld is None:
         ld = st[0] if cols else 0       # of no columns: torch has 1
+    if sh[1] < cols:
+        raise ValueError(f"{name}: rows of {cols} values are needed")
     if sh[0] < rows or sh[1] < cols + -cols % 8 or ld != st[0]:
         _holds(t, rows, cols, 8, ld)
     return t.data_ptr(), ld

@@ -75,6 +75,20 @@ def test_binding(calls):  # noqa: F811
         refused(calls, bad)
 
 
+def test_binding_refuses_reductions_past_a_view(calls):  # noqa: F811
+    """Columns behind a view's last one may hold anything: a longer reduction must not read them, where
+    they complete a piece of 8 either."""
+    x, w, y = bf16(5, 64)[:4], bf16(33, 64)[:32], bf16(4, 32)
+    taken(calls, S.nm_linear, x[:, :60], w[:, :60], y)
+    taken(calls, S.nm_linear, x[:, :60], w, y)
+    taken(calls, S.nm_linear, x, w[:, :60], y, k=60)
+    taken(calls, S.nm_linear, x, bf16(33, 32)[:32, :30], y, w_meta=i8(1, 32, 16), k=60)
+    for bad in (lambda: S.nm_linear(x, w[:, :60], y), lambda: S.nm_linear(x[:, :60], w, y, k=64),
+                lambda: S.nm_linear(x[:, :60], w[:, :60], y, k=61),
+                lambda: S.nm_linear(x, bf16(33, 32)[:32, :30], y, w_meta=i8(1, 32, 16))):
+        refused(calls, bad)
+
+
 def test_oracle():
     x, w = np.array([[1.0, 2.0], [0.0, -1.0]]), np.array([[1.0, 1.0], [2.0, -3.0], [0.0, 0.5]])
     y, size = O.linear(x, w, np.array([0.0, 1.0, -1.0]), "silu", np.ones((2, 3)))

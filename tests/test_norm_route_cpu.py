@@ -111,6 +111,18 @@ def test_norm_binding(calls):  # noqa: F811
         refused(calls, bad)
 
 
+def test_norm_binding_refuses_rows_past_a_view(calls):  # noqa: F811
+    """Columns behind a view's last one may hold anything: a longer row must not read them, where they
+    complete a piece of 8 either."""
+    x, r, q, s = bf16(5, 64)[:4], torch.zeros(5, 64)[:4], i8(4, 64), torch.zeros(4)
+    taken(calls, S.nm_rmsnorm_i8, x[:, :60], None, q, s, r[:, :60])
+    taken(calls, S.nm_rmsnorm_i8, x[:, :60], None, q, s, r)
+    taken(calls, S.nm_rmsnorm_i8, x, None, q, s, r[:, :60], k=60)
+    for bad in (lambda: S.nm_rmsnorm_i8(x, None, q, s, r[:, :60]), lambda: S.nm_rmsnorm_i8(x[:, :60], None, q, s, k=64),
+                lambda: S.nm_rmsnorm_i8(x[:, :60], None, q, s, k=61)):
+        refused(calls, bad)
+
+
 def test_route_binding(calls):  # noqa: F811
     l, ids, w = torch.zeros(4, 60), torch.zeros(4, 8, dtype=torch.int32), torch.zeros(4, 8)
     a = taken(calls, S.nm_moe_route, l, ids, w)
