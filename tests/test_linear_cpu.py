@@ -5,6 +5,7 @@ import math
 import numpy as np
 import pytest
 
+import linear_plan as P
 import oracle as O
 import semi_structured_sparse_amd as S
 from test_i8_binding_cpu import Recorder, bf16, calls, i8, refused, taken  # noqa: F401
@@ -51,6 +52,36 @@ def test_workspace_size():
     assert f(8192, 14336, 4096) == 0                               # whole tiles
     assert f(1, 64, 16384) >= 2 * 64 * 4                           # few rows, a long reduction: split
     assert f(40, 256, 14336) >= 2 * 40 * 256 * 4
+
+
+def test_plan_agrees_with_the_workspace():
+    """The tests' own account of the dispatch, by which they choose sizes: reduction ranges as the library
+    asks for them."""
+    rng = np.random.default_rng(1)
+    for _ in range(4000):
+        t, o, k = (int(2 ** rng.uniform(0, top)) for top in (12, 14, 14.5))
+        sparse = bool(rng.integers(2))
+        if sparse:
+            k = max(4, k // 4 * 4)
+        for route in (None, "few_stream", "few_tile", "tile_lds"):
+            got = S.nm_linear_workspace_size(t, o, k, sparse, S.route_bits(route) if route else 0)
+            assert got == P.workspace(t, o, k, sparse, route), (t, o, k, sparse, route)
+
+
+def test_every_instance_is_run():
+    """The sizes of test_linear_gpu.py's test_every_instance and test_rounds_of_large_tiles reach every
+    kernel that nm_linear has, split and whole, with every count of waves."""
+    few = [(1, 4, 4, False), (1, 2, 4, False), (2, 2, 4, False)]
+    for tb in (1, 2, 4):
+        few += [(tb, 1, 4, False), (tb, 1, 8, False), (tb, 1, 8, True)] + [(tb, 1, 16, False)] * (tb < 4)
+    every = {("few", *f) for f in few} | {("tile", shape, split) for shape in range(4) for split in (False, True)}
+    for sparse, sizes in ((False, P.DENSE), (True, P.SPARSE)):
+        run = {P.instance(P.plan(t, o, k, sparse, route), sparse)[1:] for t, o, k, route in sizes}
+        assert run == every, (every - run, run - every)
+        for t, o, k in P.LARGE:
+            assert P.plan(t, o, k, sparse) == ("large",)
+            bands = -(-o // 256)
+            assert bands > 8 and bands % 8 and bands * -(-t // 256) > 256
 
 
 def test_binding(calls):  # noqa: F811

@@ -5,6 +5,7 @@ import ctypes
 import numpy as np
 import pytest
 
+import linear_plan as P
 import oracle as O
 import synth
 
@@ -293,3 +294,46 @@ def test_captured_streams_and_a_shared_workspace():
     for bad in (lambda: S.nm_linear(cases[0].xd.cpu(), cases[0].wd, y), lambda: S.nm_linear(cases[0].xd, cases[0].wd, y.cpu(), stream=side)):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("sparse,size", [(False, s) for s in P.DENSE] + [(True, s) for s in P.SPARSE])
+def test_every_instance(sparse, size):
+    """Each kernel instance that the dispatch has, with outputs in rows that keep the alignment of four
+    and in rows that do not."""
+    t, o, k, route = size
+    route = {None: "auto", "few_stream": "stream"}[route]
+    plan = P.plan(*size[:3], sparse, size[3])
+    print("linear instance", sparse, size, plan, flush=True)
+    for n, (fn, kind, pad) in enumerate([("gelu", torch.bfloat16, -o % 4), ("none", torch.float32, 1 + -o % 4)]):
+        c = Case(20 + n, t, o, k, sparse=sparse, fn=fn, kind=kind)
+        c.pad = pad
+        got, taken = c.run(route)
+        assert ("few_stream" in taken) == (plan[0] == "few") and ("reduce" in taken) == (plan[-1] > 1), taken
+        c.check(got)
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+@pytest.mark.parametrize("size", P.LARGE)
+def test_rounds_of_large_tiles(sparse, size):
+    """More tiles of 256 x 256 than the chip runs at once: the call by shape against the same kernel by hint
+    (a row's bits do not depend on its place), hundreds of rows against a call of few tiles, a row of
+    every 61 against the oracle."""
+    t, o, k = size
+    assert P.plan(t, o, k, sparse) == ("large",)
+    k = k if sparse or k % 8 else k - 1                # dense: a row that ends inside a piece
+    k = k - 4 if sparse else k
+    for kind, pad in ((torch.float32, 0), (torch.bfloat16, 3)):
+        print("linear large", sparse, size, k, kind, flush=True)
+        c = Case(30, t, o, k, sparse=sparse, fn="silu", kind=kind)
+        c.pad = pad
+        got, taken = c.run("auto")
+        assert "tile_lds" in taken and "reduce" not in taken
+        assert np.array_equal(got, c.run("tile")[0])
+        rows = np.r_[0:70, 251:262, 1000:1300, 4090:4200]
+        part = Case(31, 1, 1, 4, kind=kind)
+        part.__dict__.update(c.__dict__)
+        part.t, part.x, part.xd, part.res = len(rows), c.x[rows], c.xd[torch.from_numpy(rows).cuda()].contiguous(), c.res[rows]
+        assert np.array_equal(part.run("tile")[0], got[rows])
+        rows = np.unique(np.r_[np.arange(0, t, 61), t - 1])
+        part.t, part.x, part.res = len(rows), c.x[rows], c.res[rows]
+        part.check(got[rows])
