@@ -55,7 +55,7 @@ class Case:
             self.meta = torch.zeros(max(1, S.nm_meta_block_bytes(o, k)), dtype=torch.uint8, device="cuda")
             if k and o:
                 S.nm_meta_block(dev(O.pack_meta_2bit(idx)), o, k, self.meta)
-            self.w, stored = O.expand_24_values(vals, idx, k), vals
+            self.w, stored, self.idx = O.expand_24_values(vals, idx, k), vals, idx
         else:
             self.w, self.meta = O.f32_from_bf16(synth.normal_bf16(rng, (o, k), 0.1)), None
             stored = self.w
@@ -337,3 +337,30 @@ def test_rounds_of_large_tiles(sparse, size):
         rows = np.unique(np.r_[np.arange(0, t, 61), t - 1])
         part.t, part.x, part.res = len(rows), c.x[rows], c.res[rows]
         part.check(got[rows])
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+@pytest.mark.parametrize("fn", ["none", "silu"])
+def test_infinities_and_nan_reach_what_multiplies_them(sparse, fn):
+    """A NaN or an infinity in X makes those outputs so whose weight row keeps its position, with the
+    weight's sign, and leaves the others' bits; a NaN in W its output of every token."""
+    for t, o, k in ((6, 40, 256), (40, 70, 260), (300, 300, 260)):
+        c = Case(9, t, o, k, sparse=sparse, fn=fn, kind=torch.float32)
+        kept = np.ones((o, k), bool)
+        if sparse:
+            kept = O.expand_24_values(np.ones((o, k // 2), bool), c.idx, k)
+        want = {r: c.run(r)[0] for r in ROUTES}
+        c.xd[1, 5], c.xd[4, k - 1], c.xd[2, 0] = float("nan"), float("inf"), float("-inf")
+        c.wd[7, 3] = float("nan")
+        for r in ROUTES:
+            print("linear not finite", sparse, fn, t, o, k, r, flush=True)
+            got = c.run(r)[0]
+            expect = want[r].copy()
+            expect[1, kept[:, 5]] = np.nan
+            for row, pos, sign in ((4, k - 1, 1.0), (2, 0, -1.0)):
+                v = np.where(c.w[:, pos] == 0, np.nan, np.copysign(np.inf, sign * c.w[:, pos]))
+                if fn == "silu":                                     # the limit 0 at -inf
+                    v = np.where(v == -np.inf, c.res[row], v)
+                expect[row, kept[:, pos]] = v[kept[:, pos]]
+            expect[:, 7] = np.nan
+            assert np.array_equal(got, expect, equal_nan=True)
