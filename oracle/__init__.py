@@ -859,7 +859,9 @@ def rmsnorm_i8(x: np.ndarray, residual=None, stream: str = "bf16", weight=None, 
     """fp32 values x [R][K] (+ residual) -> (codes int8 [R][K or K'], scale fp64 [R], s fp32 [R][K],
     y fp64 [R][K]).  s = x + residual rounded to the stream's type, p = fp32(s weight), codes =
     127 p / max|p| to the nearest integer, ties to even: the quotient in fp64, where a tie of
-    24-bit values is exact and everything else stays on its side (2^-25 of a unit at least).
+    24-bit values is exact and everything else stays on its side (a quotient P 2^a / (M 2^b) of
+    24-bit P and M that is no half is over 2^-32 of a unit from one, b - a being 8 at most where
+    it passes 1/2 / 127; fp64 is off by 2^-47).
     scale = max|p| / (127 rms), y = p / rms, rms = sqrt(mean s^2 + eps).  Zero rows: scale 1; rows
     with an infinity or a NaN in p: that as scale, zero codes."""
     s = np.asarray(x, np.float32)

@@ -11,8 +11,11 @@
 // quotient may fall on the wrong side of a half: t = p fp32(127 / max) is off by at most 127 *
 // 2^-23 = 1.52e-5 (the quotient and the product round once each), so a code whose t lies more
 // than 2e-5 from a half is right, and the others, one in 25000, are divided again in fp64.
-// There 127 p is exact, and since p and max are 24-bit integers times powers of two, a quotient
-// that is no half differs from one by at least 2^-25 of a unit: far more than fp64 rounds.
+// There 127 p is exact.  With p = P 2^a, max = M 2^b, P and M integers under 2^24, and a half (2 j + 1) / 2
+// the difference is (254 P - (2 j + 1) M 2^(b - a)) / (2 M 2^(b - a)): no half, its numerator is 1 at
+// least, 2 if b > a, and b - a is 8 at most where |p| passes max / 256, which every half does (1 / 254
+// of max): over 2^-32 of a unit (127 (128 n - 1) / (256 (127 n - 1)) comes that near), and an fp64
+// quotient of at most 127 is off by 2^-47.
 // The sum of squares is carried in fp64, so that no row overflows it.
 //
 // One pass: a row's p stay in registers between the reductions (the largest |p| and the sum

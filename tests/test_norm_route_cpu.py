@@ -154,6 +154,17 @@ def test_oracle_norm_codes_are_the_exact_quotient():
         assert list(y[i]) == pytest.approx([float(v) / rms for v in p], rel=1e-14)
 
 
+def test_oracle_norm_codes_next_to_a_half():
+    n = np.arange(66054, 131000, 997, dtype=np.int64)
+    for side in (-1, 1):
+        x = np.stack([256 * (127 * n + side), 128 * n + side], axis=1).astype(np.float32)
+        q, _, _, _ = O.rmsnorm_i8(x)
+        for row, code in zip(x, q):
+            exact = 127 * Fraction(float(row[1])) / Fraction(float(row[0]))
+            assert 0 < abs(exact - Fraction(1, 2)) < Fraction(1, 2 ** 30)
+            assert int(code[1]) == round(exact) == (side < 0)
+
+
 def test_oracle_norm_selection_and_rows_without_a_value():
     x = np.array([[3, -3, 1, 2, 0, 0, 0, 0], [0] * 8, [1, np.inf, 0, 0, 0, 0, 0, 0]], np.float32)
     q, scale, _, _ = O.rmsnorm_i8(x, n=1, m=4)

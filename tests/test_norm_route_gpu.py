@@ -170,6 +170,25 @@ def test_norm_borders():
     check_norm(np.stack([np.ldexp(t, e) for e in (-140, -40, -8, 0, 90)]).astype(np.float32), "f32")
 
 
+def test_norm_codes_next_to_a_half():
+    """Quotients 1/2 +- 1 / (256 M), M a 24-bit number: as near a half as codes come without being one
+    (127 (128 n -+ 1) = 128 (127 n -+ 1) +- 1), at every size."""
+    for e in (-148, -60, 0, 90):
+        for first in (66054, 99000, 131000):
+            n = first + np.arange(0, 60, 3, dtype=np.int64)
+            for side in (-1, 1):
+                if (128 * n + side).max() >= 1 << 24:
+                    continue
+                p, top = 128 * n + side, 256 * (127 * n + side)
+                assert ((127 * p - 128 * (127 * n + side)) == -side).all()
+                x = np.stack([top, p, -p], axis=1).astype(np.float64) * 2.0 ** e
+                x = np.pad(x.astype(np.float32), ((0, 0), (0, 37)))
+                assert (x[:, 1].astype(np.float64) == p * 2.0 ** e).all()
+                check_norm(x, "f32")
+                q = run_norm(x, "f32")[0]
+                assert (q[:, 0] == 127).all() and (q[:, 1] == (side < 0)).all() and (q[:, 2] == -(side < 0)).all()
+
+
 def test_norm_rows_without_a_value():
     k = 200
     x = heavy(np.random.default_rng(1), 8, k)
