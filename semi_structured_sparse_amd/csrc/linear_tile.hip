@@ -370,9 +370,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_lin_tile(
   constexpr int V_BYTES = KM * A_CHUNK;
   constexpr int A_BYTES = V_BYTES + (SP ? BM * 8 * KM : 0), B_BYTES = KM * B_CHUNK;
   constexpr int NA = BM / RPG / NW, NB = BN / 8 / NW;
-  constexpr int MROWS = BM / NW;               // rows whose positions a wave loads: 2 KM lanes each
   static_assert(NA >= 1 && NB >= 1 && BM % (RPG * NW) == 0 && BN % (8 * NW) == 0, "load groups per wave");
-  static_assert(!SP || MROWS * KM == 16 || MROWS * KM == 32, "positions: 8 KM bytes a row, 4 a lane");
+  static_assert(!SP || (KM == 2 && BM == 16 * NW), "positions: of 16 rows a wave, 16 bytes a row and step, 4 a lane");
   constexpr int A3 = NST > 3 ? A_BYTES : 16, B3 = NST > 3 ? B_BYTES : 16;
   __shared__ __align__(16) unsigned char sA0[A_BYTES], sB0[B_BYTES], sA1[A_BYTES], sB1[B_BYTES], sA2[A_BYTES], sB2[B_BYTES],
       sA3[A3], sB3[B3];
@@ -427,9 +426,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_lin_tile(
   }
   const uint8_t* mlane = nullptr;   // the lane's four bytes of positions in step 0
   if constexpr (SP) {
-    const int r = wave * MROWS + lane / (2 * KM) % MROWS;
+    const int r = wave * 16 + (lane >> 2);
     const int o = r < orows ? r : orows - 1;
-    mlane = meta + (o0 + o) * 16 + 4 * (lane % (2 * KM));
+    mlane = meta + (o0 + o) * 16 + 4 * (lane & 3);
   }
 
   f32x4 acc[FI][FJ];
@@ -450,9 +449,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_lin_tile(
         b2lds16(rw, a + c * A_CHUNK + (wave + q * NW) * 1024, aoff[q] | at, (uint32_t)(ch * AROW));
     }
     if constexpr (SP) {
-      if (MROWS * KM == 32 || lane < 32)
-        __builtin_amdgcn_global_load_lds(KM == 2 ? mlane + s * (O * 16) : mlane + (s >> 1) * (O * 16) + 8 * (s & 1),
-                                         (lds_void*)(a + V_BYTES + wave * MROWS * 8 * KM), 4, 0, 0);
+      __builtin_amdgcn_global_load_lds(mlane + s * (O * 16), (lds_void*)(a + V_BYTES + wave * 256), 4, 0, 0);
     }
 #pragma unroll
     for (int c = 0; c < KM; ++c) {
