@@ -704,8 +704,9 @@ typedef enum { NM_FN_NONE = 0, NM_FN_RELU = 1, NM_FN_SILU = 2, NM_FN_GELU_TANH =
  *   y         NM_Y_F32 or NM_Y_BF16, [t][ldy >= o]; nothing outside rows [0, t) and columns [0, o) is
  *             written
  *   workspace device scratch or NULL.  With nm_linear_workspace_size bytes the reduction may be
- *             split across workgroups; with less, the call runs unsplit.  Contents after the
- *             call are unspecified; calls sharing a workspace must be ordered.
+ *             split across workgroups; with less, the call runs unsplit (few tokens over a long
+ *             reduction: two to three times as long).  Contents after the call are unspecified;
+ *             calls sharing a workspace must be ordered.
  *   route, route_taken   as for nm_spmm_i8
  * k == 0 gives zero sums (x and w may then be NULL).  The same call on the same inputs gives the same
  * bits; routes differ in the order of their fp32 sums.  k <= NM_LINEAR_MAX_K, t and o <=

@@ -32,6 +32,15 @@ enum class Kind { kFew, kMid, kLarge };
 // 29.0 / 28.0, 16 37.9 / 29.1; 1 x 14336 x 4096 31.9 / 26.8; 8 x 256 x 2048 5.9 / 6.7, 32 9.0 / 7.0; 16 x
 // 4096 x 1024 6.5 / 6.4; 2:4 1 x 4096 x 4096 9.0 / 9.3, 4 9.7 / 9.6, 8 10.3 / 9.7; 1 x 4096 x 14336 22.0 /
 // 21.9; 1 x 14336 x 4096 22.1 / 18.9; 8 x 256 x 2048 5.7 / 6.6.
+// From 160 tiles of 256 x 256 these (us, smaller / 256 x 256 tiles; their number, bias, bf16 out, weights
+// from HBM): dense 2048 x 4096 x 4096 83 / 87 (128), 2304 x 4096 x 4096 114 / 82 (144), 2560 x 4096 x
+// 4096 116 / 84 (160), 700 x 14336 x 1024 39 / 33 (168), 3000 x 4096 x 2048 68 / 52 (192), 4096 x 4096 x
+// 4096 164 / 109 (256), 4352 x 4096 x 4096 198 / 175 (272), 1200 x 14336 x 4096 189 / 179 (280), 3000 x
+// 6144 x 4096 184 / 177 (288), 1500 x 14336 x 4096 223 / 186 (336), 2304 x 4096 x 14336 385 / 264 (144),
+// 4352 x 4096 x 14336 655 / 567 (272); 2:4 2048 x 4096 x 4096 69 / 78 (128), 2304 x 4096 x 4096 97 / 77
+// (144), 2560 x 4096 x 4096 98 / 78 (160), 700 x 14336 x 1024 36 / 31 (168), 4096 x 4096 x 4096 136 / 85
+// (256), 2560 x 7168 x 4096 154 / 137 (280), 5120 x 4096 x 4096 165 / 149 (320).  So they stay ahead where
+// a second round is mostly idle, and would be from 144 on.
 Kind plan_linear(int64_t t, int64_t o, int64_t k, bool sparse, uint32_t route) {
   if (route & NM_ROUTE_FEW_STREAM) return Kind::kFew;
   if (route & NM_ROUTE_FEW_TILE) return Kind::kMid;

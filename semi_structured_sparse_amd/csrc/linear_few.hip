@@ -258,7 +258,7 @@ FewPlan few_plan(int64_t t, int64_t o, int64_t k, bool sparse) {
   if (s > room) s = room;
   if (steps <= 8 * p.waves) s = 1;
   p.splits = s < 2 ? 1 : s > 16 ? 16 : s;
-  if (blocks <= 32 && p.splits == 1 && p.tb < 4 && steps >= 32) p.waves = 16;   // 64 KiB of partial tiles
+  if (blocks <= 32 && p.splits == 1 && p.tb < 4 && steps >= 32) p.waves = 16;   // up to 32 KiB of partial tiles
   return p;
 }
 

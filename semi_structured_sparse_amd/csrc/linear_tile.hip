@@ -596,7 +596,9 @@ __device__ __forceinline__ float acc_read(float a) {
 // gelu, and the card runs them at 1.45 GHz; the same loop with nothing but its matrix instructions
 // takes 506-528 us at 8192 x 4096 x 14336, with nothing but its loads 518-534.  Measured (cards differ
 // by 5%): 8192 x 4096 x 14336 684 us (8 waves of 64 x 128 on two stages 722), 8192 x 14336 x 4096 with
-// bias and gelu 741-780 (without 707-735), 4096 x 4096 x 4096 104 (110).
+// bias and gelu 741-780 (without 707-735), 4096 x 4096 x 4096 104 (110).  On a card where they take 692,
+// 755 (with a bias) and 110 the library's bf16 products of these sizes, which have no epilogue, take
+// 616, 667 and 95.
 __global__ __launch_bounds__(256) void k_lin_big(
     const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ w, int64_t ldw, int64_t T, int64_t O, int k,
     LinEpi epi, int tiles_m, int tiles_n, int group) {
@@ -781,7 +783,8 @@ __global__ __launch_bounds__(256) void k_lin_big(
 // The matrix pipe is busy in 44% of cycles, LDS in 24% (11% of these conflicts, in the positions), at
 // 1.78 GHz (bias and gelu, 8192 x 14336 x 4096): less than the dense product's share, since a
 // step's barrier comes after half its matrix cycles.  Measured: 8192 x 14336 x 4096 528 us (8
-// waves of 64 x 128 on two stages 656), 8192 x 4096 x 14336 504 (713), 4096 x 4096 x 4096 78 (94).
+// waves of 64 x 128 on two stages 656), 8192 x 4096 x 14336 504 (713), 4096 x 4096 x 4096 78 (94); on
+// another card 542, 519 and 87 with a bias.
 __global__ __launch_bounds__(256) void k_lin_big24(
     const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ w, int64_t ldw,
     const uint8_t* __restrict__ meta, int64_t T, int64_t O, int k, LinEpi epi, int tiles_m, int tiles_n, int group) {
@@ -1062,6 +1065,7 @@ hipError_t launch_lin_tile(const LinArgs& a, bool large, float* part, int64_t pa
   if (!large) {
     const bool sp = a.meta != nullptr;
     p = mid_plan(a.t, a.o, a.k, sp);
+    // the tile stays the split plan's (40 x 4096 x 14336 67 us, 2:4 73, with a workspace 37 and 26)
     if (part == nullptr || part_bytes < lin_mid_part_bytes(a.t, a.o, a.k, sp)) p.splits = 1;
   }
   return a.meta != nullptr ? launch_kind<true>(a, p.shape, p.splits, part, s)

@@ -501,7 +501,8 @@ hipError_t launch_moe_i8(const MoeArgs& a, void* ws, hipStream_t s) {
     // 356, 64 440 / 384 / 414; 64 tokens 6/64 4096 x 1408 217 / 227 / 285, 6/32 2048 x 1024 75 / 79 / 83,
     // 8/16 2048 x 1024 104 / 97 / 99, 2/4 4096 x 8192 205 / 177 / 165, 4/4 345 / 277 / 236; 48 tokens 8/32
     // 2048 x 1024 79 / 82 / 86; 2:4 64 tokens 2/8 4096 x 14336 323 / 281 / 403, 8/16 2048 x 1024 94 / 89 /
-    // 79, 4/4 4096 x 8192 286 / 232 / 209, 2/4 162 / 139 / 154.
+    // 79, 4/4 4096 x 8192 286 / 232 / 209, 2/4 162 / 139 / 154 (where the one rule for dense and 2:4 takes
+    // items of 64).
     const int tb = t <= 16 || t * a.top <= 12 * a.experts ? 1 : t <= 32 || t * a.top <= 20 * a.experts ? 2 : 4;
     hipError_t e;
     if (a.gate_meta != nullptr) {

@@ -15,8 +15,8 @@
 // LDS (8192 x 256, 8 of biased scores: 24.8 us instead of 11.3).
 //
 // Bound by the rounds' chains of dependent cross-lane moves, not by memory: 8192 tokens, 8 chosen,
-// 64 / 256 / 512 biased experts 6.5 / 11.3 / 21.3 us, 256 by softmax 7.8 (8.9 MB: 1.5 at the rate of
-// a large copy); 16 x 64 3.2 us, most of it the launch.
+// 64 / 256 / 512 biased experts 6.0-6.5 / 10.3-11.8 / 20-22 us, 256 by softmax 7.4-7.8 (8.9 MB: 1.5 at
+// the rate of a large copy); 16 x 64 3.0-3.2 us, most of it the launch.
 #include <type_traits>
 
 #include "layer_launch.h"
