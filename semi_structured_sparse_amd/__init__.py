@@ -797,6 +797,14 @@ def _list_of(t, n, dev, kind, name):
     return t.data_ptr()
 
 
+def _in_rows(width, *ts):
+    """Refuses matrices (not lists, not raw pointers) of other rows than `width`, whose values would be read
+    or written across them."""
+    for t in ts:
+        if t is not None and type(t) is not int and t.dim() == 2 and t.shape[1] != width:
+            raise ValueError(f"a matrix with rows of {width} values is needed, not of {t.shape[1]}")
+
+
 def _bf16_rows(t, dev, rows, cols, ld, name):
     """(pointer, leading dimension) of `rows` rows of `cols` bf16 values that are read in pieces of 8 (a
     last piece past the columns may hold anything, so none of it counts as one)."""
@@ -903,7 +911,12 @@ def nm_moe_route(logits, ids, weights, kind=NM_ROUTER_SOFTMAX, bias=None, renorm
     if experts is None:
         experts = logits.shape[1]
     if top is None:
-        top = ids.shape[1]
+        sh = ids.shape
+        top = sh[1]
+        if getattr(weights, "shape", sh) != sh:     # alike, mostly: one look
+            _in_rows(top, weights)
+    else:
+        _in_rows(top, ids, weights)
     lp, ll, _ = _rows_of(logits, dev, t, experts, 1, ldl, NM_Y_F32, "logits")
     res = lib().nm_moe_route(lp, t, experts, ll, _list_of(bias, experts, dev, _f32, "bias"), kind, top,
                              1 if renormalize else 0, scale, _list_of(ids, t * top, dev, _int32, "ids"),
@@ -959,6 +972,8 @@ def nm_moe_i8(x, x_scale, ids, weights, w_gate, gate_scale, w_up, up_scale, w_do
     if hidden is None:
         hidden = y.shape[1]
     if inter is None:
+        if w_gate.dim() != 3:
+            raise ValueError("w_gate: a matrix for each expert is needed, or inter")
         inter = w_gate.shape[1]
     sparse = gate_meta is not None
     wk, dk = (hidden // 2, inter // 2) if sparse else (hidden, inter)
@@ -966,6 +981,9 @@ def nm_moe_i8(x, x_scale, ids, weights, w_gate, gate_scale, w_up, up_scale, w_do
     a.t, a.hidden, a.inter, a.experts, a.top, a.act = t, hidden, inter, experts, top, act
     a.x, a.ldx = _codes(x, None if x is None or type(x) is int else x.shape, dev, t, hidden, ldx)
     a.x_scale = _list_of(x_scale, t, dev, _f32, "x_scale")
+    _in_rows(top, ids, weights)
+    _in_rows(inter, gate_scale, up_scale)
+    _in_rows(hidden, down_scale)
     a.ids = _list_of(ids, t * top, dev, _int32, "ids")
     a.weights = _list_of(weights, t * top, dev, _f32, "weights")
     a.w_gate, a.ldw = _expert_codes(w_gate, dev, experts, inter, wk, ldw, "w_gate")

@@ -102,6 +102,25 @@ def test_binding(calls):  # noqa: F811
         refused(calls, S.nm_moe_i8, **{**parts(True), **bad})
 
 
+def test_binding_refuses_rows_of_other_lengths(calls):  # noqa: F811
+    """Choices, weights and scales follow each other without a gap: a matrix whose rows are longer than
+    the call's would be read across them."""
+    e, h, i, t = 3, 64, 100, 4
+    parts = dict(x=i8(t, 64), x_scale=torch.zeros(t), ids=torch.zeros(t, 2, dtype=torch.int32), weights=torch.zeros(t, 2),
+                 w_gate=i8(e, i, 64), gate_scale=torch.zeros(e, i), w_up=i8(e, i, 64), up_scale=torch.zeros(e, i),
+                 w_down=i8(e, h, 112), down_scale=torch.zeros(e, h), y=bf16(t, h), workspace=i8(4096))
+    taken(calls, S.nm_moe_i8, **parts)
+    flat = {n: parts[n].reshape(-1) for n in ("ids", "weights", "gate_scale", "up_scale", "down_scale")}
+    taken(calls, S.nm_moe_i8, **{**parts, **flat}, top=2)
+    taken(calls, S.nm_moe_i8, **{**parts, "gate_scale": torch.zeros(e, i, 1), "up_scale": torch.zeros(e + 1, i)})
+    taken(calls, S.nm_moe_i8, **{**parts, "ids": torch.zeros(t + 1, 2, dtype=torch.int32)})
+    for bad in (dict(weights=torch.zeros(t, 4)), dict(ids=torch.zeros(t, 4, dtype=torch.int32)), dict(top=1),
+                dict(gate_scale=torch.zeros(e, 112)), dict(up_scale=torch.zeros(i, e)), dict(down_scale=torch.zeros(e, 112)),
+                # a matrix of all experts' rows says nothing of an expert's
+                dict(w_gate=i8(e * i, 64), w_up=i8(e * i, 64), experts=e)):
+        refused(calls, S.nm_moe_i8, **{**parts, **bad})
+
+
 def test_oracle():
     x = np.array([[1, -2], [3, 0]], np.int8)
     xs = np.array([0.5, 0.25], np.float32)

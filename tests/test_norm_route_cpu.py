@@ -136,6 +136,15 @@ def test_route_binding(calls):  # noqa: F811
         refused(calls, bad)
 
 
+def test_route_binding_refuses_rows_of_other_lengths(calls):  # noqa: F811
+    l, ids, w = torch.zeros(4, 60), torch.zeros(4, 8, dtype=torch.int32), torch.zeros(4, 8)
+    taken(calls, S.nm_moe_route, l, ids.reshape(-1), w.reshape(-1), top=8)
+    taken(calls, S.nm_moe_route, l, torch.zeros(5, 8, dtype=torch.int32), w)
+    for bad in (lambda: S.nm_moe_route(l, ids, torch.zeros(4, 16)), lambda: S.nm_moe_route(l, ids, w, top=4),
+                lambda: S.nm_moe_route(l, ids.reshape(2, 16), w, top=8)):
+        refused(calls, bad)
+
+
 # ------------------------------------------------------------------------- pins of the oracle ---
 
 def test_oracle_norm_codes_are_the_exact_quotient():
